@@ -46,6 +46,7 @@
 
 #include <math_constants.h>
 
+#include "attn_util.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
@@ -119,21 +120,6 @@ struct AttnSmem {
   uint32_t mask[kAttnMaxCands / kTile];
   uint32_t list[kAttnMaxCands];
 };
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-
-// 2^x by the MUFU.EX2 unit (ex2.approx: about 2 ulp, 2^-inf = 0); its error is far below the
-// ~2^-16 relative precision that the P_hi + P_lo pair keeps.
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 
 // Byte offset of 16-byte chunk k (0..7) of head row h in a 16 KB exchange buffer (rows of 128
 // bytes); the XOR spreads a quarter-warp's accesses over all banks.
@@ -867,13 +853,14 @@ __global__ void __launch_bounds__(kAttnCombineThreads) attn_combine_kernel(AttnC
       }
     }
   }
-  const float inv = 1.f / L;
+  const float inv = L == 0.f ? 0.f : 1.f / L;  // no candidate and no sink term: the output is zero
   float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
   const int rope0 = P.d - P.rope_dim;
-  if (dim >= rope0) {
+  if (dim + 2 >= rope0) {
     const int t = P.q_pos[qi];
 #pragma unroll
     for (int c = 0; c < 4; c += 2) {
+      if (dim + c < rope0) continue;  // rope_dim need not be a multiple of 4
       float cs, sn;
       rope_cos_sin(t, P.inv_freq[(dim + c - rope0) >> 1], &cs, &sn);
       const float e = y[c], od = y[c + 1];

@@ -47,7 +47,8 @@ typedef enum {
   CSA_ERR_CUDA = 3,          /* a CUDA runtime/driver call failed */
   CSA_ERR_TIMEOUT = 4,       /* (device status) a bounded wait inside a kernel gave up */
   CSA_ERR_WORKSPACE = 5,     /* ws is null, misaligned or smaller than csa_workspace_size */
-  CSA_ERR_BOUNDS = 6         /* (device status) an index read from memory was out of range */
+  CSA_ERR_BOUNDS = 6,        /* (device status) an index read from memory was out of range */
+  CSA_ERR_NO_PAGES = 7       /* (device status) fewer free pages than a page-table call needed */
 } csa_status;
 
 /* Text of a status code (static string). */
@@ -88,7 +89,8 @@ enum {
   CSA_WS_DECODE_FUSED = 4,
   CSA_WS_HCA_DECODE_FUSED = 5,
   CSA_WS_OUTPUT_PROJ = 6,
-  CSA_WS_Q_PROJ = 7
+  CSA_WS_Q_PROJ = 7,
+  CSA_WS_PAGES = 8           /* page-table calls: B = slots, S = max_pages, max_entries = num_pages */
 };
 
 /*
@@ -392,8 +394,124 @@ CSA_API int csa_window_projection(int M, int hidden, int d, int rope_dim, float 
                                   void* stream);
 
 /*
+ * Caches in pages (no counterpart in the pages this header cites; what a serving system needs around them: memory
+ * that grows with a request's length, prompts shared by several samples, half the bytes per entry).
+ *
+ * A page table maps each slot (request b of a call is slot b) to pages of a pool: entry e of slot r is row
+ * e % page_size of page table[r][e / page_size]; -1 is a place without a page. refs[p] counts the holders of page p
+ * (0: free): the table's places, plus whatever else the caller counts in (a prompt kept for later requests). Caches
+ * behind one table (main and index entries, every layer of a model) each have a pool of num_pages pages. Table and
+ * counts live in device memory and change in stream order; calls that share a table must be ordered.
+ *   page_size: a power of two in [16, 1024]; num_pages * page_size and slots * max_pages below 2^31.
+ *   table dev int32 [slots, max_pages]; refs dev int32 [num_pages].
+ */
+typedef struct {
+  int slots, max_pages, num_pages, page_size;
+  int32_t* table;
+  int32_t* refs;
+} csa_page_table;
+
+/*
+ * A cache behind a page table.
+ *   scales != NULL: 8 bits, d = 512. pages dev uint8 [num_pages, page_size, d] (e4m3 codes); scales dev float
+ *     [num_pages, page_size / block], one for each `block` rows (a power of two in [1, 64], at most page_size):
+ *     the value of a row is its codes times its block's scale. csa_cache_append writes powers of two, which leave
+ *     every value exact in bf16; the attention calls take any positive normal scales (0: the rows do not count).
+ *   scales == NULL: bf16 rows, pages dev uint16 [num_pages, page_size, d], d a multiple of 8 up to 512, block unused.
+ * pages must be 16-byte aligned.
+ */
+typedef struct {
+  int d, block;
+  void* pages;
+  float* scales;
+} csa_paged_cache;
+
+/*
+ * csa_cache_append -- the entries that a segment of S tokens completes, from `rows` (where csa_compress leaves them: entry g
+ * of request b at rows + b*rows_bstride + g*d; one such buffer serves every layer in turn) into the pages. For
+ * request b these are entries start_pos[b]/ratio .. (start_pos[b]+S)/ratio - 1; a negative start_pos marks a
+ * request to skip. 8-bit caches: a block's scale becomes the least power of two 2^k (k >= -100) with max |x| <= 448 * 2^k over its
+ * rows, and never less than it was while the block has earlier rows (rows of entries below start_pos/ratio), whose codes are
+ * rounded again if it grows. Each value is rounded to the nearest code. A row with a value that is not finite makes its
+ * block's scale NaN (and the block's later readers NaN). Pages of the entries must be mapped and not shared with
+ * another slot; an entry whose page is not mapped, or whose g >= max_rows, is left out and records CSA_ERR_BOUNDS.
+ *   start_pos dev int32 [B]; rows dev bf16, 16-byte aligned, rows_bstride a multiple of 8.
+ *   ws: at least 256 bytes (status word), as in csa_cache_read.
+ */
+CSA_API int csa_cache_append(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int ratio,
+                             const int32_t* start_pos, const uint16_t* rows, int64_t rows_bstride, int max_rows,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * csa_cache_read -- entries idx[b, i] of each request as bf16: out[b, i, :] = code * scale (exact for power-of-two scales). An
+ * index of -1 leaves its row of `out` as it was; one whose page is not mapped does too, and records CSA_ERR_BOUNDS.
+ *   idx dev int32 [B, n]; out dev bf16 [B, n, d], 16-byte aligned.
+ */
+CSA_API int csa_cache_read(const csa_page_table* pt, const csa_paged_cache* cache, int B, int n, const int32_t* idx,
+                           uint16_t* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * csa_pages_reserve -- pages for entries[r] entries of every slot r: each place below ceil(entries[r] / page_size) without a page gets
+ * one, the lowest free pages in (slot, place) order, with refs 1. Places that have a page keep it.
+ * csa_pages_fork -- slot r becomes a copy of slot parent[r] (all slots at once; parent[r] == r: unchanged, -1: emptied, its pages
+ * freed). entries[s] is the number of entries of slot s that its copies take over. Full pages are shared (refs counts
+ * them); of a last page that is partly filled one heir keeps the original (slot s itself if it stays, else its lowest copy)
+ * and every other copy gets a page of its own, the lowest free ones in slot order, into which the page is copied in every cache
+ * given. So rows appended after a fork never meet another slot's.
+ * csa_pages_compact -- the L live pages (refs > 0) become pages 0 .. L-1: the k-th live page at or behind L moves to the
+ * k-th free page before L, in every cache given. map[p] = where page p is now, -1 if it was free; *live = L.
+ * If a value of the table or the arguments is out of range (CSA_ERR_BOUNDS; compact: the one place is left as it is) or the
+ * free pages do not suffice (CSA_ERR_NO_PAGES), the code is recorded in the status word and reserve and fork change nothing.
+ *   entries, parent dev int32 [slots]; map dev int32 [num_pages]; live dev int32 [1].
+ *   caches: host array of n_caches; every cache behind the table whose rows are to follow (0 .. 1024).
+ *   ws/ws_bytes: workspace of at least csa_workspace_size(CSA_WS_PAGES, slots, max_pages, num_pages, 0). Its contents do not
+ *   outlive a call (but for the status word), so one workspace serves calls that are ordered on a stream.
+ */
+CSA_API int csa_pages_reserve(const csa_page_table* pt, const int32_t* entries, void* ws, size_t ws_bytes,
+                              void* stream);
+CSA_API int csa_pages_fork(const csa_page_table* pt, const csa_paged_cache* caches, int n_caches,
+                           const int32_t* parent, const int32_t* entries, void* ws, size_t ws_bytes, void* stream);
+CSA_API int csa_pages_compact(const csa_page_table* pt, const csa_paged_cache* caches, int n_caches, int32_t* map,
+                              int32_t* live, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * csa_indexer_scores_paged / csa_indexer_topk_paged -- csa_indexer_scores / csa_indexer_topk over a bf16 cache in pages (d = 128).
+ * max_entries is max_pages * page_size: scores dev float [B, S, max_pages * page_size]. A visible entry whose page is not
+ * mapped scores 0 and records CSA_ERR_BOUNDS. Workspaces: csa_workspace_size(CSA_WS_SPARSE_ATTN, ...) and
+ * csa_workspace_size(CSA_WS_INDEXER_TOPK, B, S, max_pages * page_size, topk).
+ */
+CSA_API int csa_indexer_scores_paged(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int H_I,
+                                     int ratio, const int32_t* q_pos, const uint16_t* q_idx, const float* w,
+                                     float* scores, void* ws, size_t ws_bytes, void* stream);
+CSA_API int csa_indexer_topk_paged(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int H_I,
+                                   int ratio, int topk, const int32_t* q_pos, const uint16_t* q_idx, const float* w,
+                                   int32_t* topk_idx, float* scores_opt, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * csa_sparse_attn8 / hca_attn8 -- csa_sparse_attn / hca_attn over an 8-bit cache in pages: the entries count with
+ * their dequantised values, the window rows stay bf16. csa_sparse_attn8 takes the entries of topk_idx (-1: none); hca_attn8
+ * every entry s < (t+1)/ratio, any number of them. A negative q_pos marks a padding query: its output is zero. A query
+ * with no candidate has output zero too.
+ *   ring, q, sink, out, rope and scale as in csa_sparse_attn; d = 512, 1 <= H <= 128, rope_dim even and <= 128,
+ *   window in [1, 1024], topk in [1, 2048]; ring_bstride a multiple of 8; ring_cap >= window + S - 1 for the
+ *   rows of a segment's queries to be all there (the caller's choice, not checked).
+ *   ws: csa_workspace_size(CSA_WS_SPARSE_ATTN, ...) / CSA_WS_HCA_ATTN, or only its status word (slower for few queries).
+ * A selected entry that is not visible at t, a visible one (range form) beyond the table, or an entry whose page is
+ * not mapped is skipped and records CSA_ERR_BOUNDS.
+ */
+CSA_API int csa_sparse_attn8(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int H, int rope_dim,
+                             float rope_base, float scale, int ratio, const int32_t* q_pos, const uint16_t* q,
+                             const uint16_t* ring, int64_t ring_bstride, int ring_cap, int window,
+                             const int32_t* topk_idx, int topk, const float* sink, void* out, int out_is_f32, void* ws,
+                             size_t ws_bytes, void* stream);
+CSA_API int hca_attn8(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int H, int rope_dim,
+                      float rope_base, float scale, int ratio, const int32_t* q_pos, const uint16_t* q,
+                      const uint16_t* ring, int64_t ring_bstride, int ring_cap, int window, const float* sink,
+                      void* out, int out_is_f32, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * csa_get_device_status -- synchronise `stream`, read the status word in `ws` into *status
- * (CSA_OK, CSA_ERR_TIMEOUT or CSA_ERR_BOUNDS) and clear it. Returns CSA_ERR_CUDA if the
+ * (CSA_OK, CSA_ERR_TIMEOUT, CSA_ERR_BOUNDS or CSA_ERR_NO_PAGES) and clear it. Returns CSA_ERR_CUDA if the
  * stream itself reports an error.
  */
 CSA_API int csa_get_device_status(void* ws, void* stream, int* status);

@@ -20,6 +20,7 @@ CSA_ERR_CUDA = 3
 CSA_ERR_TIMEOUT = 4
 CSA_ERR_WORKSPACE = 5
 CSA_ERR_BOUNDS = 6
+CSA_ERR_NO_PAGES = 7
 
 CSA_WS_INDEXER_TOPK = 1
 CSA_WS_SPARSE_ATTN = 2
@@ -28,6 +29,7 @@ CSA_WS_DECODE_FUSED = 4
 CSA_WS_HCA_DECODE_FUSED = 5
 CSA_WS_OUTPUT_PROJ = 6
 CSA_WS_Q_PROJ = 7
+CSA_WS_PAGES = 8
 
 
 class CompressorCfg(ctypes.Structure):
@@ -66,6 +68,19 @@ class HcaDecodeArgs(ctypes.Structure):
     ]
 
 
+class PageTableArg(ctypes.Structure):
+    """Mirror of csa_page_table."""
+    _fields_ = [("slots", c_int), ("max_pages", c_int), ("num_pages", c_int), ("page_size", c_int),
+                ("table", c_void_p), ("refs", c_void_p)]
+
+
+class PagedCacheArg(ctypes.Structure):
+    """Mirror of csa_paged_cache."""
+    _fields_ = [("d", c_int), ("block", c_int), ("pages", c_void_p), ("scales", c_void_p)]
+
+
+_PT, _PC = POINTER(PageTableArg), POINTER(PagedCacheArg)
+
 # name -> (restype, argtypes)
 PROTOTYPES = {
     "csa_status_string": (c_char_p, [c_int]),
@@ -101,6 +116,21 @@ PROTOTYPES = {
                                  c_void_p]),
     "csa_window_projection": (c_int, [c_int, c_int, c_int, c_int, c_float, c_void_p, c_void_p, c_void_p, c_void_p,
                                       c_void_p, c_size_t, c_void_p]),
+    "csa_cache_append": (c_int, [_PT, _PC, c_int, c_int, c_int, c_void_p, c_void_p, c_int64, c_int, c_void_p, c_size_t,
+                                 c_void_p]),
+    "csa_cache_read": (c_int, [_PT, _PC, c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "csa_pages_reserve": (c_int, [_PT, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "csa_pages_fork": (c_int, [_PT, _PC, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "csa_pages_compact": (c_int, [_PT, _PC, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "csa_indexer_scores_paged": (c_int, [_PT, _PC, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                                         c_void_p, c_size_t, c_void_p]),
+    "csa_indexer_topk_paged": (c_int, [_PT, _PC, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "csa_sparse_attn8": (c_int, [_PT, _PC, c_int, c_int, c_int, c_int, c_float, c_float, c_int, c_void_p, c_void_p,
+                                 c_void_p, c_int64, c_int, c_int, c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p,
+                                 c_size_t, c_void_p]),
+    "hca_attn8": (c_int, [_PT, _PC, c_int, c_int, c_int, c_int, c_float, c_float, c_int, c_void_p, c_void_p, c_void_p,
+                          c_int64, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
 }
 
 _lib = None

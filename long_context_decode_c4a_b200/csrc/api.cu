@@ -16,6 +16,7 @@
 #include <utility>
 
 #include "csa.h"
+#include "host.cuh"
 #include "kernels.cuh"
 
 namespace csa {
@@ -23,6 +24,8 @@ namespace csa {
 namespace {
 
 thread_local char g_err[512] = "";
+
+}  // namespace
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -32,22 +35,7 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
-#define CSA_CHECK_ARG(cond, ...)                                   \
-  do {                                                             \
-    if (!(cond)) return fail(CSA_ERR_INVALID_ARG, __VA_ARGS__);    \
-  } while (0)
-#define CSA_CHECK_SUP(cond, ...)                                   \
-  do {                                                             \
-    if (!(cond)) return fail(CSA_ERR_UNSUPPORTED, __VA_ARGS__);    \
-  } while (0)
-#define CSA_CUDA(call)                                                                     \
-  do {                                                                                     \
-    cudaError_t e_ = (call);                                                               \
-    if (e_ != cudaSuccess) return fail(CSA_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_)); \
-  } while (0)
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+namespace {
 
 // ---- TMA descriptors through the runtime's driver entry point (no link-time libcuda).
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -85,29 +73,7 @@ int make_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows
   return CSA_OK;
 }
 
-struct DeviceInfo {
-  int sms = 0;
-  int max_smem = 0;
-  bool attrs_set = false;
-};
-
-// Launch with programmatic stream serialization: the kernel may begin launching while the
-// previous kernel on the stream runs; it calls pdl_wait() before touching global memory.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                       Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
+}  // namespace
 
 int device_info(DeviceInfo** out) {
   static DeviceInfo info[64];
@@ -127,6 +93,7 @@ int device_info(DeviceInfo** out) {
       return fail(CSA_ERR_UNSUPPORTED, "libcsa is built for sm_100a; device is sm_%d%d", cc_major, cc_minor);
     const int ms = d.max_smem;
     CSA_CUDA(cudaFuncSetAttribute(attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
+    CSA_CUDA(cudaFuncSetAttribute(attn8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
     CSA_CUDA(cudaFuncSetAttribute(gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
     CSA_CUDA(cudaFuncSetAttribute(indexer_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
     CSA_CUDA(cudaFuncSetAttribute(indexer_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
@@ -139,6 +106,8 @@ int device_info(DeviceInfo** out) {
   *out = &d;
   return CSA_OK;
 }
+
+namespace {
 
 // ---- workspace layout
 struct IdxWs {
@@ -164,11 +133,15 @@ IdxWs indexer_ws_layout(long long queries, int max_entries, int topk, bool with_
   return w;
 }
 
+}  // namespace
+
 int check_ws(const void* ws, size_t ws_bytes, size_t need) {
   if (ws == nullptr || !aligned(ws, 256)) return fail(CSA_ERR_WORKSPACE, "workspace null or not 256-byte aligned");
   if (ws_bytes < need) return fail(CSA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
   return CSA_OK;
 }
+
+namespace {
 
 int check_cfg(const csa_compressor_cfg* c) {
   CSA_CHECK_ARG(c != nullptr, "cfg is null");
@@ -257,6 +230,7 @@ struct IndexerArgs {
   float* scores_opt;
   void* ws;
   size_t ws_bytes;
+  const csa_page_table* pt = nullptr;  // index entries in pages (idx_cache: the pool, idx_bstride unused)
 };
 
 int check_indexer_args(const IndexerArgs& a, bool scores = true, bool select = true) {
@@ -280,10 +254,10 @@ int check_indexer_args(const IndexerArgs& a, bool scores = true, bool select = t
   CSA_CHECK_ARG(aligned(a.q_idx, 16) && aligned(a.idx_cache, 16) && aligned(a.w, 4) && aligned(a.topk_idx, 4) &&
                     aligned(a.q_pos, 4),
                 "misaligned pointer");
-  CSA_CHECK_ARG(a.idx_bstride >= (int64_t)a.max_entries * a.d_I && a.idx_bstride % a.d_I == 0,
+  CSA_CHECK_ARG(a.pt != nullptr || (a.idx_bstride >= (int64_t)a.max_entries * a.d_I && a.idx_bstride % a.d_I == 0),
                 "idx_bstride must be >= max_entries*d_I and a multiple of d_I");
   CSA_CHECK_ARG(a.scores_opt == nullptr || aligned(a.scores_opt, 4), "scores_opt misaligned");
-  const long long rows = (long long)a.B * (a.idx_bstride / a.d_I);
+  const long long rows = a.pt ? 0 : (long long)a.B * (a.idx_bstride / a.d_I);
   CSA_CHECK_SUP(rows < (1ll << 31), "index cache too large for 32-bit row coordinates");
   const long long qrows = (long long)a.B * a.S * a.H_I;
   CSA_CHECK_SUP(qrows < (1ll << 31), "too many query rows");
@@ -336,7 +310,17 @@ int run_indexer_topk(const IndexerArgs& a, cudaStream_t st, cudaEvent_t const* e
     P.status = status;
 
     CUtensorMap map_k, map_q;
-    if (int rc = make_map_2d(&map_k, a.idx_cache, 128, (uint64_t)a.B * P.rows_per_req, 128, 64, 128)) return rc;
+    uint64_t k_rows = (uint64_t)a.B * P.rows_per_req;
+    uint32_t k_box = 128;
+    if (a.pt != nullptr) {
+      P.table = a.pt->table;
+      P.max_pages = a.pt->max_pages;
+      P.num_pages = a.pt->num_pages;
+      P.page_shift = log2_int(a.pt->page_size);
+      k_rows = (uint64_t)a.pt->num_pages * a.pt->page_size;
+      k_box = (uint32_t)std::min(128, a.pt->page_size);
+    }
+    if (int rc = make_map_2d(&map_k, a.idx_cache, 128, k_rows, 128, 64, k_box)) return rc;
     if (int rc = make_map_2d(&map_q, a.q_idx, 128, (uint64_t)queries * a.H_I, 128, 64, (uint32_t)P.N)) return rc;
     const size_t smem = indexer_smem_bytes(stages, P.N, fused);
     const dim3 grid((unsigned)std::min<long long>(P.total_items, dev->sms));
@@ -415,6 +399,8 @@ struct AttnArgs {
 // B200's 148 SMs); a launch uses no more splits than its device's pairs and its workspace allow.
 constexpr int kAttnSplitPairs = 74;
 
+}  // namespace
+
 int attn_ws_splits(long long queries) {
   if (queries <= 0) return 1;
   return (int)std::max<long long>(1, std::min<long long>(kAttnMaxSplits, kAttnSplitPairs / queries));
@@ -424,6 +410,8 @@ size_t attn_part_bytes(long long queries, int splits) {
   if (splits <= 1) return 0;
   return (size_t)queries * splits * (128 * 512 + 2 * 128) * sizeof(float);
 }
+
+namespace {
 
 int check_attn_args(const AttnArgs& a, bool csa_mode) {
   CSA_CHECK_ARG(a.B > 0 && a.S > 0, "B and S must be positive");
@@ -575,6 +563,7 @@ const char* csa_status_string(int status) {
     case CSA_ERR_TIMEOUT: return "device wait timed out";
     case CSA_ERR_WORKSPACE: return "workspace missing or too small";
     case CSA_ERR_BOUNDS: return "index out of range";
+    case CSA_ERR_NO_PAGES: return "not enough free pages";
     default: return "unknown status";
   }
 }
@@ -604,6 +593,10 @@ int csa_workspace_size(int kind, int B, int S, int max_entries, int topk, size_t
       *bytes = kStatusBytes + attn_part_bytes(q, attn_ws_splits(q));
       return CSA_OK;
     }
+    case CSA_WS_PAGES:
+      CSA_CHECK_SUP((long long)B * S < (1ll << 31), "page table too large");
+      *bytes = pages_ws_bytes(B, S, max_entries);
+      return CSA_OK;
     case CSA_WS_OUTPUT_PROJ:
     case CSA_WS_Q_PROJ:
       *bytes = kStatusBytes;
@@ -681,6 +674,26 @@ int hca_attn(int B, int S, int H, int d, int rope_dim, float rope_base, float sc
              cache_bstride, max_entries, nullptr, 0, sink, out, out_is_f32, ws, ws_bytes};
   if (int rc = check_attn_args(a, false)) return rc;
   return run_attn(a, false, static_cast<cudaStream_t>(stream));
+}
+
+int csa_indexer_scores_paged(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int H_I, int ratio,
+                             const int32_t* q_pos, const uint16_t* q_idx, const float* w, float* scores, void* ws,
+                             size_t ws_bytes, void* stream) {
+  if (int rc = check_paged(pt, cache, B, false)) return rc;
+  IndexerArgs a{B, S, H_I, cache->d, ratio, 1, q_pos, q_idx, w, static_cast<const uint16_t*>(cache->pages), 0,
+                pt->max_pages * pt->page_size, nullptr, scores, ws, ws_bytes, pt};
+  if (int rc = check_indexer_args(a, true, false)) return rc;
+  return run_indexer_topk(a, static_cast<cudaStream_t>(stream), nullptr, true, false);
+}
+
+int csa_indexer_topk_paged(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int H_I, int ratio,
+                           int topk, const int32_t* q_pos, const uint16_t* q_idx, const float* w, int32_t* topk_idx,
+                           float* scores_opt, void* ws, size_t ws_bytes, void* stream) {
+  if (int rc = check_paged(pt, cache, B, false)) return rc;
+  IndexerArgs a{B, S, H_I, cache->d, ratio, topk, q_pos, q_idx, w, static_cast<const uint16_t*>(cache->pages), 0,
+                pt->max_pages * pt->page_size, topk_idx, scores_opt, ws, ws_bytes, pt};
+  if (int rc = check_indexer_args(a)) return rc;
+  return run_indexer_topk(a, static_cast<cudaStream_t>(stream));
 }
 
 int csa_output_projection(int M, int G, int Kg, int R, int D, const uint16_t* o, const uint16_t* wo_a,

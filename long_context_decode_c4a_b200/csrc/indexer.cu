@@ -266,10 +266,26 @@ __global__ void __launch_bounds__(kIdxThreads, 1)
           if (vis > 0 && c.et == (vis - 1) / 128 && !wait_flag_and_clear(&F.flags[c.b], abort_flag, status, 204)) break;
         }
         mbar_arrive_expect_tx(&sm.k_full[st], 32768);
-        const int krow = (int)((long long)c.b * P.rows_per_req + (long long)c.et * 128);
         uint8_t* dst = k_tiles + (size_t)st * 32768;
-        tma_load_2d(dst, &map_k, 0, krow, &sm.k_full[st]);
-        tma_load_2d(dst + 16384, &map_k, 64, krow, &sm.k_full[st]);
+        if (P.table == nullptr) {
+          const int krow = (int)((long long)c.b * P.rows_per_req + (long long)c.et * 128);
+          tma_load_2d(dst, &map_k, 0, krow, &sm.k_full[st]);
+          tma_load_2d(dst + 16384, &map_k, 64, krow, &sm.k_full[st]);
+        } else {
+          // One box per page of the tile. A page that is not mapped is loaded as the rows behind the pool, which
+          // TMA fills with zeros; it counts as an error where a visible entry lies on it.
+          const int box = min(128, 1 << P.page_shift);
+          for (int r = 0; r < 128; r += box) {
+            const int e = c.et * 128 + r;
+            const int lp = e >> P.page_shift;
+            const int pg = lp < P.max_pages ? P.table[(long long)c.b * P.max_pages + lp] : -1;
+            const bool ok = pg >= 0 && pg < P.num_pages;
+            if (!ok && e < iter.gv) record_status(status, CSA_DEV_BOUNDS);
+            const int krow = (ok ? pg : P.num_pages) * (1 << P.page_shift) + (e & ((1 << P.page_shift) - 1));
+            tma_load_2d(dst + r * 128, &map_k, 0, krow, &sm.k_full[st]);
+            tma_load_2d(dst + 16384 + r * 128, &map_k, 64, krow, &sm.k_full[st]);
+          }
+        }
         trace_mark(status, 0, (uint32_t)(100 + n));
         if (n < 100) trace_time(status, 600 + (int)n);
         ++n;

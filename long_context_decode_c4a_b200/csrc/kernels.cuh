@@ -71,6 +71,10 @@ struct IndexerParams {
   float* scores;                          // [B*S, scores_stride]
   long long scores_stride;
   uint32_t* status;
+  // Index entries in pages (null: contiguous per request): entry e of request b is row e % page_size of page
+  // table[b*max_pages + e / page_size]. A tile is loaded in boxes of min(128, page_size) rows.
+  const int32_t* table;
+  int max_pages, num_pages, page_shift;
 };
 
 // The decode step's compression, run by the indexer (csa_decode_fused): the epilogue warps of CTA c
@@ -169,6 +173,120 @@ struct AttnCombineParams {
 };
 
 __global__ void attn_combine_kernel(AttnCombineParams P);
+
+// ------------------------------------------------------------------------------ attention over 8-bit pages
+
+constexpr int kAttn8Threads = 480;        // warps 0..3 gathers, 4-5 score MMAs, 6 PV MMAs, 7..14 softmax
+
+struct Attn8Params {
+  int B, S, H, rope_dim;
+  float scale_log2;                       // scale * log2(e)
+  double inv_freq[kMaxRopePairs];         // rope_base^(-2i/rope_dim), formed on the host in double
+  int window, ring_cap;
+  long long ring_bstride;
+  const uint16_t* ring;                   // slot j of request b at ring + b*ring_bstride + j*512
+  const uint8_t* pages;                   // e4m3 [num_pages, 1 << page_shift, 512]
+  const float* scales;                    // [num_pages, (1 << page_shift) >> block_shift]
+  const int32_t* table;                   // [B.., max_pages]: page of each run of 1 << page_shift entries
+  int num_pages, page_shift, block_shift, max_pages;
+  int max_entries, ratio;                 // max_entries = max_pages << page_shift
+  const int32_t* q_pos;                   // [B*S]; negative: a padding query
+  const uint16_t* q;                      // [B*S, H, 512]
+  const int32_t* topk_idx;                // [B*S, topk]; null: every visible entry
+  int topk;
+  const float* sink;                      // [H]
+  void* out;                              // [B*S, H, 512]
+  int out_is_f32;
+  uint32_t* status;
+  int splits;                             // as AttnParams: partials [item, H, 512] and [item, 2, H]
+  float* part_o;
+  float* part_ml;
+};
+
+__global__ void attn8_kernel(Attn8Params P);
+size_t attn8_smem_bytes();
+
+// ------------------------------------------------------------------------------ caches in pages
+
+constexpr int kAppendThreads = 512;
+constexpr int kAppendMaxUnit = 64;        // entries a CTA of the e4m3 append takes: max(block, 16)
+
+struct AppendParams {
+  int S, ratio;
+  const int32_t* start_pos;               // [B]; negative: a padding request
+  const uint16_t* rows;                   // entry g of request b at rows + b*rows_bstride + g*d
+  long long rows_bstride;
+  int max_rows, d;
+  uint8_t* pages;
+  float* scales;
+  const int32_t* table;
+  int num_pages, page_shift, block_shift, max_pages, unit;
+  uint32_t* status;
+};
+
+__global__ void cache_append_kernel(AppendParams P);
+__global__ void cache_append_bf16_kernel(AppendParams P);
+
+constexpr int kReadThreads = 256;
+
+struct ReadParams {
+  int B, n, d;
+  const int32_t* idx;                     // [B, n]
+  const uint8_t* pages;
+  const float* scales;                    // null: bf16 pages
+  const int32_t* table;
+  int num_pages, page_shift, block_shift, max_pages;
+  uint16_t* out;                          // [B, n, d]
+  uint32_t* status;
+};
+
+__global__ void cache_read_kernel(ReadParams P);
+
+constexpr int kPagesCluster = 8;          // CTAs of a page-table operation
+constexpr int kPagesThreads = 1024;
+
+struct PagesParams {
+  int slots, max_pages, num_pages, page_shift;
+  int32_t* table;                         // [slots, max_pages]
+  int32_t* refs;                          // [num_pages]
+  const int32_t* entries;                 // [slots]
+  const int32_t* parent;                  // fork: [slots]
+  int32_t* map;                           // compact: [num_pages]
+  int32_t* live;                          // compact: [1]
+  // workspace
+  int* counts;                            // [3, kPagesCluster]
+  int* n_moves;
+  int* list_a;                            // [num_pages]
+  int* list_b;                            // [num_pages]
+  int* move_src;                          // [num_pages]
+  int* move_dst;
+  int* heir;                              // [slots]
+  int* rows;                              // [slots, max_pages]
+  uint32_t* status;
+};
+
+__global__ void pages_reserve_kernel(PagesParams P);
+__global__ void pages_fork_kernel(PagesParams P);
+__global__ void pages_compact_kernel(PagesParams P);
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyChunk = 16384;         // bytes a CTA copies at a time
+constexpr int kMaxCaches = 64;            // caches behind one table that a call moves (two pools each)
+
+struct PagePool {
+  uint8_t* base;
+  int page_bytes, units;                  // units = chunks of a page
+};
+
+struct CopyParams {
+  const int* n_moves;
+  const int* move_src;
+  const int* move_dst;
+  int units_per_page;
+  PagePool pool[2 * kMaxCaches];
+};
+
+__global__ void pages_copy_kernel(CopyParams P);
 
 // ------------------------------------------------------------------------------ output projection
 

@@ -9,6 +9,7 @@ namespace csa {
 constexpr uint32_t CSA_DEV_OK = 0;
 constexpr uint32_t CSA_DEV_TIMEOUT = 4;
 constexpr uint32_t CSA_DEV_BOUNDS = 6;
+constexpr uint32_t CSA_DEV_NO_PAGES = 7;
 
 // A bounded wait gives up after this many SM clock cycles (about half a second at the
 // B200's clocks), records CSA_DEV_TIMEOUT and lets the kernel unwind.

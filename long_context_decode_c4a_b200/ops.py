@@ -17,7 +17,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import CompressorCfg, DecodeArgs, HcaDecodeArgs, check
+from ._lib import CompressorCfg, DecodeArgs, HcaDecodeArgs, PagedCacheArg, PageTableArg, check
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -489,6 +489,269 @@ def window_projection(x: torch.Tensor, wkv: torch.Tensor, pos: torch.Tensor, rop
                                             wkv.data_ptr(), win.data_ptr(), ws.data_ptr(), ws.numel(), _stream()),
           "csa_window_projection")
     return win
+
+
+# ------------------------------------------------------------------------------------------------ caches in pages
+
+
+def _same_device(device: torch.device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {t.device} and {device} in one call")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}: make it the current device (torch.cuda.device) for the call")
+
+
+class PageTable:
+    """Pages of the caches behind it: slot r (request r of a call) holds entry e in row e % page_size of page
+    table[r, e // page_size] (-1: no page). refs[p] counts the holders of page p, 0: free. Both live on the GPU and change in
+    stream order; a workspace for the page-table calls (with the device status word of every call behind the
+    table) is kept beside them."""
+
+    def __init__(self, table: torch.Tensor, refs: torch.Tensor, page_size: int):
+        _need(table, "table", torch.int32)
+        _need(refs, "refs", torch.int32)
+        if table.dim() != 2 or refs.dim() != 1:
+            raise ValueError("table must be [slots, max_pages] and refs [num_pages]")
+        if page_size < 16 or page_size > 1024 or page_size & (page_size - 1):
+            raise ValueError("page_size must be a power of two in [16, 1024]")
+        if refs.device != table.device:
+            raise ValueError("table and refs must be on one device")
+        self.table, self.refs, self.page_size = table, refs, page_size
+        self.slots, self.max_pages = table.shape
+        self.num_pages = refs.shape[0]
+        self.max_entries = self.max_pages * page_size
+        self.device = table.device
+        self.ws = workspace(_lib.CSA_WS_PAGES, self.slots, self.max_pages, self.num_pages, 0, table.device)
+        self._arg = PageTableArg(self.slots, self.max_pages, self.num_pages, page_size, table.data_ptr(), refs.data_ptr())
+        self._ref = ctypes.byref(self._arg)
+
+    @classmethod
+    def empty(cls, slots: int, max_pages: int, num_pages: int, page_size: int = 64, device="cuda") -> "PageTable":
+        """A table of empty slots over free pages."""
+        return cls(torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(num_pages, dtype=torch.int32, device=device), page_size)
+
+
+class PagedCache:
+    """A cache behind a page table: pages [num_pages, page_size, 512] of e4m3 codes with scales [num_pages,
+    page_size // block] (fp32, one per block of rows), or pages [num_pages, page_size, d] of bf16 rows without scales."""
+
+    def __init__(self, book: PageTable, pages: torch.Tensor, scales: Optional[torch.Tensor] = None):
+        if pages.dim() != 3 or pages.shape[0] != book.num_pages or pages.shape[1] != book.page_size:
+            raise ValueError(f"pages must be [{book.num_pages}, {book.page_size}, d], got {tuple(pages.shape)}")
+        block = 0
+        if scales is None:
+            _need(pages, "pages", torch.bfloat16)
+        else:
+            _need(pages, "pages", torch.float8_e4m3fn, (book.num_pages, book.page_size, 512))
+            _need(scales, "scales", torch.float32)
+            if scales.dim() != 2 or scales.shape[0] != book.num_pages or scales.shape[1] < 1 or \
+                    book.page_size % scales.shape[1]:
+                raise ValueError("scales must be [num_pages, page_size // block]")
+            block = book.page_size // scales.shape[1]
+            if block > 64 or block & (block - 1):
+                raise ValueError("a block must be a power of two of at most 64 rows")
+        if pages.device != book.device or (scales is not None and scales.device != book.device):
+            raise ValueError("the cache must be on its page table's device")
+        self.book, self.pages, self.scales, self.block, self.d = book, pages, scales, block, pages.shape[2]
+        self._arg = PagedCacheArg(self.d, block, pages.data_ptr(), _ptr(scales))
+        self._ref = ctypes.byref(self._arg)
+
+    @classmethod
+    def e4m3(cls, book: PageTable, block: int = 16) -> "PagedCache":
+        """An 8-bit cache of 512-wide entries with a scale for each `block` of them."""
+        return cls(book, torch.zeros(book.num_pages, book.page_size, 512, dtype=torch.float8_e4m3fn, device=book.device),
+                   torch.zeros(book.num_pages, book.page_size // block, device=book.device))
+
+    @classmethod
+    def bf16(cls, book: PageTable, d: int = 128) -> "PagedCache":
+        """A bf16 cache of d-wide entries (the index cache)."""
+        return cls(book, torch.zeros(book.num_pages, book.page_size, d, dtype=torch.bfloat16, device=book.device))
+
+
+def _cache_list(book: PageTable, caches):
+    arr = (PagedCacheArg * max(1, len(caches)))()
+    for i, c in enumerate(caches):
+        if c.book is not book:
+            raise ValueError("a cache behind another page table")
+        arr[i] = c._arg
+    return arr
+
+
+def cache_append(cache: PagedCache, start_pos: torch.Tensor, S: int, rows: torch.Tensor, ratio: int) -> None:
+    """Write the entries that a segment of S tokens at start_pos [B] completes from rows [B, max_rows, d] bf16 (entry
+    g in row g, where compress() leaves it) into the cache's pages; start_pos < 0 skips a request. Quantises
+    into an 8-bit cache, whose blocks' scales grow as needed. The status word is in cache.book.ws."""
+    book = cache.book
+    _need(start_pos, "start_pos", torch.int32)
+    B = start_pos.shape[0]
+    if start_pos.dim() != 1 or rows.dim() != 3 or rows.shape[0] != B or rows.shape[2] != cache.d:
+        raise ValueError(f"start_pos must be [B] and rows [B, max_rows, {cache.d}]")
+    if rows.dtype != torch.bfloat16:
+        raise TypeError(f"rows must be {torch.bfloat16}, got {rows.dtype}")
+    _same_device(book.device, start_pos, rows)
+    check(_lib.load().csa_cache_append(book._ref, cache._ref, B, S, ratio, start_pos.data_ptr(), rows.data_ptr(),
+                                       _bstride(rows, "rows"), rows.shape[1], book.ws.data_ptr(), book.ws.numel(),
+                                       _stream()), "csa_cache_append")
+
+
+def cache_read(cache: PagedCache, idx: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Entries idx [B, n] (int32; -1 leaves its row of `out` as it was: zeros if not given) as bf16 [B, n, d]."""
+    book = cache.book
+    _need(idx, "idx", torch.int32)
+    if idx.dim() != 2:
+        raise ValueError("idx must be [B, n]")
+    B, n = idx.shape
+    if out is None:
+        out = torch.zeros(B, n, cache.d, dtype=torch.bfloat16, device=idx.device)
+    _need(out, "out", torch.bfloat16, (B, n, cache.d))
+    _same_device(book.device, idx, out)
+    check(_lib.load().csa_cache_read(book._ref, cache._ref, B, n, idx.data_ptr(), out.data_ptr(), book.ws.data_ptr(),
+                                     book.ws.numel(), _stream()), "csa_cache_read")
+    return out
+
+
+def pages_reserve(book: PageTable, entries: torch.Tensor) -> None:
+    """Map pages for entries[r] (int32 [slots]) entries of every slot: the lowest free pages, in slot order."""
+    _need(entries, "entries", torch.int32, (book.slots,))
+    _same_device(book.device, entries)
+    check(_lib.load().csa_pages_reserve(book._ref, entries.data_ptr(), book.ws.data_ptr(), book.ws.numel(), _stream()),
+          "csa_pages_reserve")
+
+
+def pages_fork(book: PageTable, caches, parent: torch.Tensor, entries: torch.Tensor) -> None:
+    """Slot r becomes a copy of the first entries[parent[r]] entries of slot parent[r] (its own number: unchanged,
+    -1: freed), all slots at once: full pages shared, a partly filled last page copied in every cache of `caches`
+    (all behind `book`). parent, entries: int32 [slots]."""
+    _need(parent, "parent", torch.int32, (book.slots,))
+    _need(entries, "entries", torch.int32, (book.slots,))
+    _same_device(book.device, parent, entries)
+    check(_lib.load().csa_pages_fork(book._ref, _cache_list(book, caches), len(caches), parent.data_ptr(),
+                                     entries.data_ptr(), book.ws.data_ptr(), book.ws.numel(), _stream()),
+          "csa_pages_fork")
+
+
+def pages_compact(book: PageTable, caches, map: Optional[torch.Tensor] = None, live: Optional[torch.Tensor] = None):
+    """Move the live pages to the front in every cache of `caches`. Returns (map int32 [num_pages]: where each page is
+    now, -1 if it was free; live int32 [1]: how many live)."""
+    if map is None:
+        map = torch.empty(book.num_pages, dtype=torch.int32, device=book.device)
+    if live is None:
+        live = torch.empty(1, dtype=torch.int32, device=book.device)
+    _need(map, "map", torch.int32, (book.num_pages,))
+    _need(live, "live", torch.int32, (1,))
+    _same_device(book.device, map, live)
+    check(_lib.load().csa_pages_compact(book._ref, _cache_list(book, caches), len(caches), map.data_ptr(),
+                                        live.data_ptr(), book.ws.data_ptr(), book.ws.numel(), _stream()),
+          "csa_pages_compact")
+    return map, live
+
+
+def _paged_indexer_args(q_pos, q_idx, w, cache):
+    B, S, H_I, d_I = q_idx.shape
+    if cache.scales is not None or cache.d != d_I:
+        raise ValueError(f"the index cache must hold bf16 rows of {d_I}")
+    _need(q_pos, "q_pos", torch.int32, (B, S))
+    _need(q_idx, "q_idx", torch.bfloat16)
+    _need(w, "w", torch.float32, (B, S, H_I))
+    return B, S, H_I
+
+
+def indexer_scores_paged(q_pos: torch.Tensor, q_idx: torch.Tensor, w: torch.Tensor, cache: PagedCache, ratio: int = 4,
+                         scores: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """indexer_scores() over a bf16 cache in pages: scores [B, S, max_pages * page_size] fp32."""
+    B, S, H_I = _paged_indexer_args(q_pos, q_idx, w, cache)
+    book = cache.book
+    if scores is None:
+        scores = torch.empty(B, S, book.max_entries, dtype=torch.float32, device=q_idx.device)
+    _need(scores, "scores", torch.float32, (B, S, book.max_entries))
+    if ws is None:
+        ws = workspace(_lib.CSA_WS_SPARSE_ATTN, B, S, 1, 1, q_idx.device)
+    _same_device(book.device, q_pos, q_idx, w, scores, ws)
+    check(_lib.load().csa_indexer_scores_paged(book._ref, cache._ref, B, S, H_I, ratio, q_pos.data_ptr(),
+                                               q_idx.data_ptr(), w.data_ptr(), scores.data_ptr(), ws.data_ptr(),
+                                               ws.numel(), _stream()), "csa_indexer_scores_paged")
+    return scores
+
+
+def indexer_topk_paged(q_pos: torch.Tensor, q_idx: torch.Tensor, w: torch.Tensor, cache: PagedCache, topk: int,
+                       ratio: int = 4, topk_idx: Optional[torch.Tensor] = None, scores: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """indexer_topk() over a bf16 cache in pages."""
+    B, S, H_I = _paged_indexer_args(q_pos, q_idx, w, cache)
+    book = cache.book
+    if topk_idx is None:
+        topk_idx = torch.empty(B, S, topk, dtype=torch.int32, device=q_idx.device)
+    _need(topk_idx, "topk_idx", torch.int32, (B, S, topk))
+    if scores is not None:
+        _need(scores, "scores", torch.float32, (B, S, book.max_entries))
+    if ws is None:
+        ws = workspace(_lib.CSA_WS_INDEXER_TOPK, B, S, book.max_entries, topk, q_idx.device)
+    _same_device(book.device, q_pos, q_idx, w, topk_idx, scores, ws)
+    check(_lib.load().csa_indexer_topk_paged(book._ref, cache._ref, B, S, H_I, ratio, topk, q_pos.data_ptr(),
+                                             q_idx.data_ptr(), w.data_ptr(), topk_idx.data_ptr(), _ptr(scores),
+                                             ws.data_ptr(), ws.numel(), _stream()), "csa_indexer_topk_paged")
+    return topk_idx
+
+
+def _attn8_common(q_pos, q, ring, cache, sink, out):
+    B, S, H, d = q.shape
+    if cache.scales is None or d != 512:
+        raise ValueError("attention over an 8-bit cache of rows of 512 (PagedCache with scales)")
+    _need(q_pos, "q_pos", torch.int32, (B, S))
+    _need(q, "q", torch.bfloat16)
+    _need(sink, "sink", torch.float32, (H,))
+    if ring.dtype != torch.bfloat16 or not ring.is_cuda:
+        raise TypeError("ring must be a bf16 CUDA tensor")
+    if ring.dim() != 3 or ring.shape[0] != B or ring.shape[2] != d:
+        raise ValueError(f"ring must be [{B}, ring_cap, {d}]")
+    if out is None:
+        out = torch.empty(B, S, H, d, dtype=torch.bfloat16, device=q.device)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out must be bf16 or fp32")
+    _need(out, "out", out.dtype, (B, S, H, d))
+    return B, S, H, out
+
+
+def sparse_attn8(q_pos: torch.Tensor, q: torch.Tensor, ring: torch.Tensor, cache: PagedCache, topk_idx: torch.Tensor,
+                 sink: torch.Tensor, window: int, ratio: int = 4, out: Optional[torch.Tensor] = None,
+                 scale: Optional[float] = None, rope_dim: int = 64, rope_base: float = 10000.0,
+                 ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """sparse_attn() over an 8-bit cache in pages: window rows (ring [B, ring_cap, 512] bf16) and the selected entries
+    (topk_idx [B, S, k]). q_pos < 0 marks a padding query (output zero)."""
+    B, S, H, out = _attn8_common(q_pos, q, ring, cache, sink, out)
+    _need(topk_idx, "topk_idx", torch.int32)
+    if topk_idx.dim() != 3 or topk_idx.shape[:2] != (B, S):
+        raise ValueError("topk_idx must be [B, S, k]")
+    scale = 1.0 / math.sqrt(512) if scale is None else scale
+    if ws is None:
+        ws = workspace(_lib.CSA_WS_SPARSE_ATTN, B, S, 1, 1, q.device)
+    book = cache.book
+    _same_device(book.device, q_pos, q, ring, topk_idx, sink, out, ws)
+    check(_lib.load().csa_sparse_attn8(book._ref, cache._ref, B, S, H, rope_dim, rope_base, scale, ratio,
+                                       q_pos.data_ptr(), q.data_ptr(), ring.data_ptr(), _bstride(ring, "ring"),
+                                       ring.shape[1], window, topk_idx.data_ptr(), topk_idx.shape[2], sink.data_ptr(),
+                                       out.data_ptr(), int(out.dtype == torch.float32), ws.data_ptr(), ws.numel(),
+                                       _stream()), "csa_sparse_attn8")
+    return out
+
+
+def hca_attn8(q_pos: torch.Tensor, q: torch.Tensor, ring: torch.Tensor, cache: PagedCache, sink: torch.Tensor,
+              window: int, ratio: int = 128, out: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+              rope_dim: int = 64, rope_base: float = 10000.0, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """hca_attn() over an 8-bit cache in pages: window rows plus every visible entry s < (t+1)//ratio, any number."""
+    B, S, H, out = _attn8_common(q_pos, q, ring, cache, sink, out)
+    scale = 1.0 / math.sqrt(512) if scale is None else scale
+    if ws is None:
+        ws = workspace(_lib.CSA_WS_HCA_ATTN, B, S, 1, 1, q.device)
+    book = cache.book
+    _same_device(book.device, q_pos, q, ring, sink, out, ws)
+    check(_lib.load().hca_attn8(book._ref, cache._ref, B, S, H, rope_dim, rope_base, scale, ratio, q_pos.data_ptr(),
+                                q.data_ptr(), ring.data_ptr(), _bstride(ring, "ring"), ring.shape[1], window,
+                                sink.data_ptr(), out.data_ptr(), int(out.dtype == torch.float32), ws.data_ptr(),
+                                ws.numel(), _stream()), "hca_attn8")
+    return out
 
 
 def device_status(ws: torch.Tensor) -> int:

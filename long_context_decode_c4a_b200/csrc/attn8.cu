@@ -17,9 +17,9 @@
 //     sum of the two columns, its P stands in both.
 //   P = p1 + p2: p1 is P rounded to e4m3 (4 significant bits), p2 the remainder rounded to e5m2 (3 bits), so
 //     P is off by at most 2^-8 of itself (p1 leaves 2^-4, p2 leaves 2^-4 of that: a step below a bf16 P's
-//     2^-9), or by 2^-22 of the row's running maximum where that is more: e5m2's smallest step is 2^-7 of
-//     e4m3's, which keeps a long flat tail behind one large weight (an e4m3 p2 would round each weight below
-//     2^-15 of the maximum to nothing; thousands of entries of that size are a weight to be counted).
+//     2^-9). Where p1 is subnormal (P below 2^-14, a weight below 2^-9 of the row's largest), it is off by at most
+//     2^-22 and 2^-4 of itself (2^-17 of the largest weight); a long flat tail behind one large weight is
+//     still there: e5m2 reaches 2^-24, 7 bits below e4m3.
 // P carries the scale of its column (O += (p_j s_j) c_j), so the running maximum is that of
 // y_j = l_j + log2 s_j; the denominator takes P back to p_j with 1 / s_j. The sink enters at the end
 // only: it must not push P below e4m3's range.
@@ -27,14 +27,14 @@
 // Layout: two CTAs per query; CTA `half` accumulates O[:, 256 half .. 256 half + 256) (128 heads x 256
 // columns of fp32 are half of TMEM) and computes the scores over all 512 dims itself. Both CTAs so gather
 // whole rows: 512 bytes, as many as the half row of a bf16 cache, and no partial score crosses the pair.
-//   TMEM (512 columns): [0,128) q1 (four e4m3 values a column); [128,192) and [192,256) two 64-column
-//     score tiles, whose first 32 columns P (p1, then p2) takes over; [256,512) O.
+//   TMEM (512 columns): [0,128) q1 (four codes a column); [128,192) the scores of a 64-row tile; [192,224)
+//     and [224,256) P of even and odd tiles (p1, then p2); [256,512) O. The scores leave for registers as soon
+//     as they are there, so the score MMAs of the next tile run during the softmax of this one.
 //   SMEM: four 32 KB stages of 64 rows (four 128-byte blocks in the 128B-swizzled layout, which serves the
-//     scores as a K-major and PV as an MN-major operand); q2 (64 KB); the candidate list.
-//   Warps: 0..3 build the list, split window rows and gather entries (16-byte cp.async, a warp covering
-//     one row an instruction); 4 and 5 issue the score MMAs of even and odd tiles, 6 the PV MMAs (and owns
-//     TMEM); 7..10 and 11..14 are the softmax groups of even and odd tiles, one head (TMEM lane) a
-//     thread; both first split q, and share the epilogue.
+//     scores as a K-major and PV as an MN-major operand); q2 (64 KB).
+//   Warps: 0..3 split window rows and gather entries (16-byte cp.async, a warp covering one row an
+//     instruction); 4 issues the score MMAs, 5 the PV MMAs (and owns TMEM); 6..9 and 10..13 are the softmax groups
+//     of even and odd tiles, one head (TMEM lane) a thread; both first split q, and share the epilogue.
 // Split-candidate mode (few queries): as in attn.cu; attn_combine_kernel merges the partials.
 
 #include <cuda_fp16.h>
@@ -52,9 +52,9 @@ namespace csa {
 namespace {
 
 constexpr int kProd = 128;                      // warps 0..3
-constexpr int kQkWarp = 4;                      // warps 4, 5
-constexpr int kPvWarp8 = 6;
-constexpr int kSoftWarp = 7;                    // warps 7..10 (even tiles), 11..14 (odd tiles)
+constexpr int kQkWarp = 4;
+constexpr int kPvWarp8 = 5;
+constexpr int kSoftWarp = 6;                    // warps 6..9 (even tiles), 10..13 (odd tiles)
 constexpr int kGroup = 128;                     // threads of a softmax group
 constexpr int kRows = 64;                       // rows of a tile
 constexpr int kWinRows = 32;                    // window candidates of a tile (two rows each)
@@ -63,79 +63,104 @@ constexpr uint32_t kBlk = kRows * 128;          // one 128-dim block of a stage
 constexpr uint32_t kStage = 4 * kBlk;           // 32 KB
 constexpr uint32_t kQBlk = 128 * 128;           // one 128-dim block of a q piece
 constexpr uint32_t kQ2Bytes = 4 * kQBlk;        // 64 KB
-constexpr uint32_t kRowPitch = 512 + 16;        // output staging: 256 bf16 dims, padded against bank conflicts
-// P is formed relative to 2^(m + kHead): a later row may exceed the maximum that P refers to by 2^kHead
-// before O is rescaled, and P (at most 1 = e4m3 code value 256 after the shift by 2^8) stays in range.
-constexpr float kHead = 3.f;
+// TMEM columns.
+constexpr uint32_t kScoreCol = 128, kPCol = 192, kOCol = 256;
+// P is formed relative to 2^(m + kHead), m the running maximum when O was last rescaled: later rows may exceed m
+// by 2^(kHead + kOver) before O has to be rescaled again, P staying at or below 1.75 (e4m3's 448).
+constexpr float kHead = 4.25f, kOver = 0.75f;
 static_assert(kAttn8Threads == 32 * (kSoftWarp + 8), "warp roles");
 
 struct Smem8 {
   uint64_t kv_full[kStages8], kv_free[kStages8];
-  uint64_t s_full[2];      // scores of tile j written (score tile j % 2)
-  uint64_t s_free[2];      // PV(j) completed: score tile j % 2 (scores, then P) is free, O holds PV(0..j)
-  uint64_t p_full[2];      // P of tile j stored
+  uint64_t s_full[2];      // the scores of tile j are written (barrier j % 2: a group looks at its own tiles only)
+  uint64_t s_free;         // ... and have left for registers (phase j)
+  uint64_t p_full[2];      // P of tile j stored (P buffer j % 2)
+  uint64_t pv_done[4];     // PV(j) completed (barrier j % 4): its P buffer is free, O holds PV(0..j)
   uint64_t q_done;         // q1 is in TMEM, q2 in shared memory, the staging area (stages 2, 3) is free
   uint64_t list_ready;
   uint64_t hand[2][4];     // softmax group g published the running maximum after its tile (quadrant q)
-  uint64_t drain[3];
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag, bad, epi_bad;
-  int n_tiles, tile0, win_tiles;
-  uint32_t scan[kProd / 32];
+  int n_tiles, tile0, entry_tiles;
+  int last[kProd / 32];
   float rope_cs[kMaxRopePairs][2];
   float qf[128];           // per head: 2^k_h * scale * log2(e)
   float m_hand[4][32];
   float l_g[2][128], m_g[2][128];
   float scale[kStages8][kRows];                       // the rows' scales, as gathered
   alignas(16) float col_a[8][kRows], col_k[8][kRows], col_i[8][kRows];  // (read four at a time) per softmax warp: s_j, log2 s_j, 1 / s_j of its tile's columns
-  int32_t list[kAttnMaxTopk];                         // list form: pool rows of the selected entries
 };
 
+static_assert(128 * (1024 + 16) <= kStages8 * kStage + kQ2Bytes, "output staging");
 static_assert(offsetof(Smem8, col_a) % 16 == 0 && sizeof(Smem8::col_a[0]) % 16 == 0, "float4 reads of the column factors");
 
-// 8-bit pieces of two fp32 values (|x| <= 448): hi in e4m3, the remainder lo in e5m2 or e4m3. Through fp16, which
-// holds every bf16 value scaled into e4m3's range exactly (below 2^-14: to 2^-25).
-template <bool kLoE5M2>
-__device__ __forceinline__ void split_fp8x2(float x0, float x1, uint16_t& hi, uint16_t& lo) {
-  uint32_t h, back, r;
-  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(x0), "f"(x1));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(h));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(back));
-  if (kLoE5M2) asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r));
-  else asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r));
+// The upper bytes of two fp16 pairs (their e5m2 codes, the lower bits dropped).
+__device__ __forceinline__ uint32_t codes_e5m2(uint32_t v0, uint32_t v1) { return __byte_perm(v0, v1, 0x7531); }
+
+// 2^8 (a - b) of two fp16 pairs; exact where the difference is.
+__device__ __forceinline__ uint32_t rest2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x5C005C00u));
+  return r;
+}
+// Round an fp16 pair to e4m3's 4 significant bits (half a unit away from zero: the code's carry is fp16's).
+__device__ __forceinline__ uint32_t round_e4m3(uint32_t h) { return (h + 0x00400040u) & 0xFF80FF80u; }
+
+// The larger magnitude of two bf16 pairs, the sign undefined; NaN wins.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
-// Split of a 512-dim bf16 row held by a warp: lane l has dims [8 l, 8 l + 8) in a and [256 + 8 l, ...) in b.
-// Returns 2^k with max |x| <= 448 * 2^k (k >= -100), or NaN (and zero pieces) if a value is not finite.
+// Split of a 512-dim bf16 row held by a warp: lane l has dims [8 l, 8 l + 8) in a and [256 + 8 l, ...) in b. The row
+// is scaled to at most 448 in magnitude and taken through fp16, which holds every scaled bf16 value above 2^-14
+// exactly and the rest to 2^-25. Returns 2^k with max |x| <= 448 * 2^k (k >= -100), or NaN if a value is not finite (its
+// pieces are then whatever they are: a row's scale, or a head's factor, of NaN makes NaN of all that it meets).
+// Two integer instructions in three run at half rate here, the conversions to 8 bits at a quarter: a row costs a
+// warp about 200 cycles, which is what the split of q and of the window rows is bound by.
 struct RowPieces {
   uint2 hi[2], lo[2];
 };
 template <bool kLoE5M2>
 __device__ __forceinline__ float split_row(const uint4& a, const uint4& b, RowPieces& out) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t mx = 0;
+  uint32_t mx = w[0];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) mx = __vmaxu2(mx, w[i] & 0x7FFF7FFFu);
-  mx = max(mx & 0xFFFFu, mx >> 16);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int i = 1; i < 8; ++i) mx = max_abs_bf16x2(mx, w[i]);
+  mx = __reduce_max_sync(0xffffffffu, max(mx & 0x7FFFu, (mx >> 16) & 0x7FFFu));
   const int e = (int)(mx >> 7);  // biased exponent of the largest magnitude; 448 = 1.75 * 2^8, 0x60 / 128 = 0.75
   const int k = max(-100, e - 127 - 8 + ((mx & 0x7Fu) > 0x60u ? 1 : 0));
-  const bool fin = e < 255;
-  const float inv = fin ? __uint_as_float((uint32_t)(127 - k) << 23) : 0.f;
-  uint16_t h[8], l[8];
+  const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
+  uint16_t h[8];
+  uint32_t r[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
-    split_fp8x2<kLoE5M2>(fin ? x0 * inv : 0.f, fin ? x1 * inv : 0.f, h[i], l[i]);
+    uint32_t v, back;
+    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(v) : "f"(__uint_as_float(w[i] << 16) * inv), "f"(__uint_as_float(w[i] & 0xFFFF0000u) * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h[i]) : "r"(v));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h[i]));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(v), "r"(back));
   }
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {
+  for (int v = 0; v < 2; ++v)
     out.hi[v] = make_uint2(h[4 * v] | ((uint32_t)h[4 * v + 1] << 16), h[4 * v + 2] | ((uint32_t)h[4 * v + 3] << 16));
-    out.lo[v] = make_uint2(l[4 * v] | ((uint32_t)l[4 * v + 1] << 16), l[4 * v + 2] | ((uint32_t)l[4 * v + 3] << 16));
+  if (kLoE5M2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] += 0x00800080u;  // round the byte that leaves
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      out.lo[v] = make_uint2(codes_e5m2(r[4 * v], r[4 * v + 1]), codes_e5m2(r[4 * v + 2], r[4 * v + 3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h[i]) : "r"(r[i]));
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      out.lo[v] = make_uint2(h[4 * v] | ((uint32_t)h[4 * v + 1] << 16), h[4 * v + 2] | ((uint32_t)h[4 * v + 3] << 16));
   }
-  return fin ? __uint_as_float((uint32_t)(127 + k) << 23) : CUDART_NAN_F;
+  return e < 255 ? __uint_as_float((uint32_t)(127 + k) << 23) : CUDART_NAN_F;
 }
 
 // Store lane l's 8 + 8 codes of row `row` into a [4 blocks][rows][128 B] swizzled region of block size `blk`.
@@ -146,26 +171,66 @@ __device__ __forceinline__ void store_codes(uint8_t* base, uint32_t blk, int row
     *reinterpret_cast<uint2*>(base + (uint32_t)(2 * i + (lane >> 4)) * blk + off) = v[i];
 }
 
-// 2^8 (a - b) of two fp16 pairs; exact where the difference is.
-__device__ __forceinline__ uint32_t rest2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x5C005C00u));
-  return r;
+// Two 512-dim bf16 rows of a warp, as split_row takes them.
+struct RowPair {
+  uint4 a[2], c[2];
+};
+__device__ __forceinline__ void read_row(RowPair& r, int i, const uint16_t* src, bool valid) {
+  r.a[i] = r.c[i] = make_uint4(0, 0, 0, 0);
+  if (valid) {
+    r.a[i] = reinterpret_cast<const uint4*>(src)[lane_id()];
+    r.c[i] = reinterpret_cast<const uint4*>(src)[32 + lane_id()];
+  }
 }
 
-// P (fp32 in [0, 1], standing for 2^8 P in 8-bit units) to its two pieces, four columns at a time. An fp16
-// value below 2 shifted right by 7 is the e4m3 code of 2^8 times it (same mantissa alignment, exponent
-// biases 15 and 7), subnormals included: p1 is the code of P rounded at that bit. The remainder is exact in
-// fp16; the upper byte of an fp16 value is its e5m2 code, rounded by adding half a step of the lower byte.
-__device__ __forceinline__ void split_p(const float* p, uint32_t& p1, uint32_t& p2) {
+// P (fp32 in [0, 1.75), standing for 2^8 P in 8-bit units) to its two pieces, four columns at a time.
+__device__ __forceinline__ void split_p(float p0, float p1, float p2, float p3, uint32_t& c1, uint32_t& c2) {
   uint32_t h0, h1;
-  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h0) : "f"(p[0]), "f"(p[1]));
-  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h1) : "f"(p[2]), "f"(p[3]));
-  const uint32_t a0 = (h0 + 0x00400040u) & 0xFF80FF80u, a1 = (h1 + 0x00400040u) & 0xFF80FF80u;
-  const uint32_t r0 = rest2(h0, a0) + 0x00800080u, r1 = rest2(h1, a1) + 0x00800080u;
-  p1 = __byte_perm(a0 >> 7, a1 >> 7, 0x6420);
-  p2 = __byte_perm(r0, r1, 0x7531);
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h0) : "f"(p0), "f"(p1));
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h1) : "f"(p2), "f"(p3));
+  const uint32_t a0 = round_e4m3(h0), a1 = round_e4m3(h1);
+  c1 = __byte_perm(a0 >> 7, a1 >> 7, 0x6420);  // P >= 0: no sign to move
+  c2 = codes_e5m2(rest2(h0, a0) + 0x00800080u, rest2(h1, a1) + 0x00800080u);
+}
+
+// Order of a query's tiles: up to two entry tiles first, whose gathers are quick, then window and entry tiles in turn while
+// both last: the split of a window tile takes the gathering warps longer than the tensor cores need for a tile.
+// (It also spreads the window over the splits of a query.) Returns the index of tile p among those of its kind.
+__device__ __forceinline__ int tile_of(int p, int Tw, int Te, bool& win) {
+  const int e0 = min(Te, 2), both = min(Tw, Te - e0), q = p - e0;
+  win = false;
+  if (q < 0) return p;
+  if (q < 2 * both) {
+    win = (q & 1) == 0;
+    return win ? q >> 1 : e0 + (q >> 1);
+  }
+  win = Tw > both;
+  return win ? q - both : p - both;
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 }  // namespace
@@ -191,15 +256,16 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
       mbar_init(&sm.kv_full[i], kProd);
       mbar_init(&sm.kv_free[i], 1);
     }
+    mbar_init(&sm.s_free, kGroup);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_free[i], 1);
       mbar_init(&sm.p_full[i], kGroup);
       for (int q = 0; q < 4; ++q) mbar_init(&sm.hand[i][q], 32);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&sm.pv_done[i], 1);
     mbar_init(&sm.q_done, 2 * kGroup);
     mbar_init(&sm.list_ready, 1);
-    for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.drain[i], 1);
     sm.abort_flag = 0;
     sm.bad = 0;
     sm.epi_bad = 0;
@@ -223,13 +289,92 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
   const int ecap = t < 0 ? 0 : min((int)(((long long)t + 1) / P.ratio), P.max_entries);
 
   if (warp < kProd / 32) {
-    // ------------------------------------------------------------ candidate list, window split, gathers
+    // ------------------------------------------------------------ window split, gathers
     const int pt = threadIdx.x;
     const int32_t* table = P.table + (long long)b * P.max_pages;
     const uint16_t* ring = P.ring + (long long)b * P.ring_bstride;
+    const int32_t* sel = P.topk_idx == nullptr ? nullptr : P.topk_idx + (long long)qi * P.topk;
     bool bad = false;
-    // Pool row of entry e (0 <= e < ecap), or -1 when its page is not mapped.
+    // This warp's window candidates: rows 8 warp .. 8 warp + 7 of every window tile, read two at a time and three
+    // reads ahead, across tiles. (Straight code for all eight rows is slower: a warp cannot fetch it fast enough.)
+    auto window_row = [&](int u) -> int { return (u >> 3) * kWinRows + 8 * warp + (u & 7); };
+    RowPair w0, w1, w2;
+    auto window_read = [&](RowPair& w, int u) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = window_row(u + i);
+        read_row(w, i, ring + (long long)((p0 + (k < nwin ? k : 0)) % P.ring_cap) * 512, k < nwin);
+      }
+    };
+    // Window tile w into `stage`: candidate r of the tile in rows r and r + 32.
+    auto window_store = [&](int w, int stage) {
+      uint8_t* st = stages + (size_t)stage * kStage;
+#pragma unroll 1
+      for (int u = 8 * w; u < 8 * w + 8; u += 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * warp + (u & 7) + i;
+          RowPieces pc;
+          const float s = split_row<false>(w0.a[i], w0.c[i], pc);
+          store_codes(st, kBlk, r, lane, pc.hi);
+          store_codes(st, kBlk, r + kWinRows, lane, pc.lo);
+          if (lane == 0) sm.scale[stage][r] = sm.scale[stage][r + kWinRows] = (w * kWinRows + r < nwin) ? s : 0.f;
+        }
+        w0 = w1;
+        w1 = w2;
+        window_read(w2, u + 6);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sm.kv_full[stage]);
+    };
+    auto window_begin = [&](int w) {
+      window_read(w0, 8 * w);
+      window_read(w1, 8 * w + 2);
+      window_read(w2, 8 * w + 4);
+    };
+    // Number of candidates: up to the last valid place of the list (-1 in between is a masked row), or every entry.
+    int n = ecap;
+    if (sel != nullptr) {
+      int last = 0;
+      for (int j = pt; j < P.topk; j += kProd)
+        if (sel[j] >= 0) last = j + 1;
+      last = t < 0 ? 0 : __reduce_max_sync(0xffffffffu, last);
+      if (lane == 0) sm.last[warp] = last;
+      named_bar_sync(2, kProd);
+      n = max(max(sm.last[0], sm.last[1]), max(sm.last[2], sm.last[3]));
+    } else {
+      bad = t >= 0 && ((long long)t + 1) / P.ratio > P.max_entries;
+    }
+    const int Te = (n + kRows - 1) / kRows, Jq = Tw + Te;
+    const int tile0 = (int)(((long long)Jq * sp) / P.splits);
+    const int J = (int)(((long long)Jq * (sp + 1)) / P.splits) - tile0;
+    if (pt == 0) {
+      sm.n_tiles = J;
+      sm.tile0 = tile0;
+      sm.entry_tiles = Te;
+      mbar_arrive(&sm.list_ready);
+    }
+    // The first window tile of this CTA is read now, each next one as the one before is stored.
+    {
+      bool win = false;
+      int w = 0;
+      for (int j = 0; j < J && !win; ++j) w = tile_of(tile0 + j, Tw, Te, win);
+      if (win) window_begin(w);
+    }
+
+    // Lane i < 16 of a warp has the tile's row warp + 4 i: its entry is read two tiles ahead, its page one tile ahead.
+    auto entry_of = [&](int j) -> int {
+      bool win;
+      const int k = tile_of(tile0 + j, Tw, Te, win) * kRows + warp + 4 * (lane & 15);
+      if (j >= J || win || k >= n) return -1;
+      return sel != nullptr ? sel[k] : k;
+    };
     auto pool_row = [&](int e) -> int {
+      if (e < 0) return -1;
+      if (e >= ecap) {
+        bad = true;
+        return -1;
+      }
       const int pg = table[e >> P.page_shift];
       if (pg < 0 || pg >= P.num_pages) {
         bad = true;
@@ -237,111 +382,21 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
       }
       return (pg << P.page_shift) | (e & ((1 << P.page_shift) - 1));
     };
-    // Window tile w of the query into `stage`: candidate r of the tile in rows r and r + 32.
-    auto window_tile = [&](int w, int stage) {
-      uint8_t* st = stages + (size_t)stage * kStage;
-#pragma unroll 1
-      for (int r0 = 0; r0 < 8; r0 += 4) {
-        uint4 a[4], c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * warp + r0 + i, k = w * kWinRows + r;
-          a[i] = c[i] = make_uint4(0, 0, 0, 0);
-          if (k < nwin) {
-            const uint4* src = reinterpret_cast<const uint4*>(ring + (long long)((p0 + k) % P.ring_cap) * 512);
-            a[i] = src[lane];
-            c[i] = src[32 + lane];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * warp + r0 + i;
-          RowPieces pc;
-          const float s = split_row<false>(a[i], c[i], pc);
-          store_codes(st, kBlk, r, lane, pc.hi);
-          store_codes(st, kBlk, r + kWinRows, lane, pc.lo);
-          if (lane == 0) sm.scale[stage][r] = sm.scale[stage][r + kWinRows] = (w * kWinRows + r < nwin) ? s : 0.f;
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&sm.kv_full[stage]);
-    };
-    // One pair per query: its first two tiles (stages 0 and 1) are window tiles and need no list.
-    int done = 0;
-    if (P.splits == 1)
-      for (; done < min(Tw, 2); ++done) window_tile(done, done);
-
-    int n;  // entries
-    if (P.topk_idx != nullptr) {
-      // Each thread takes a contiguous run of the selection; runs are compacted in order.
-      const int32_t* sel = P.topk_idx + (long long)qi * P.topk;
-      const int per = (P.topk + kProd - 1) / kProd;
-      const int lo = min(P.topk, pt * per), hi = min(P.topk, lo + per);
-      int rows[kAttnMaxTopk / kProd];
-      uint32_t cnt = 0;
-#pragma unroll
-      for (int u = 0; u < kAttnMaxTopk / kProd; ++u) {
-        const int j = lo + u;
-        const int s = (u < per && j < hi) ? sel[j] : -1;
-        bad |= s >= ecap;
-        rows[u] = (s >= 0 && s < ecap) ? s : -1;
-      }
-#pragma unroll
-      for (int u = 0; u < kAttnMaxTopk / kProd; ++u) {
-        if (rows[u] >= 0) rows[u] = pool_row(rows[u]);
-        cnt += rows[u] >= 0 ? 1u : 0u;
-      }
-      uint32_t inc = cnt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) sm.scan[warp] = inc;
-      named_bar_sync(2, kProd);
-      uint32_t pos = inc - cnt, total = 0;
-#pragma unroll
-      for (int i = 0; i < kProd / 32; ++i) {
-        pos += i < warp ? sm.scan[i] : 0u;
-        total += sm.scan[i];
-      }
-#pragma unroll
-      for (int u = 0; u < kAttnMaxTopk / kProd; ++u)
-        if (rows[u] >= 0) sm.list[pos++] = rows[u];
-      n = (int)total;
-    } else {
-      n = ecap;
-      bad = t >= 0 && ((long long)t + 1) / P.ratio > P.max_entries;
-    }
-    const int Jq = Tw + (n + kRows - 1) / kRows;
-    const int tile0 = (int)(((long long)Jq * sp) / P.splits);
-    const int J = (int)(((long long)Jq * (sp + 1)) / P.splits) - tile0;
-    named_bar_sync(2, kProd);  // the list is complete
-    if (pt == 0) {
-      sm.n_tiles = J;
-      sm.tile0 = tile0;
-      sm.win_tiles = Tw;
-      mbar_arrive(&sm.list_ready);
-    }
-
-    // Lane i < 16 of a warp holds the pool row of the tile's row warp + 4 i, fetched one tile ahead.
-    auto fetch = [&](int j) -> int {
-      const int k = (tile0 + j - Tw) * kRows + warp + 4 * (lane & 15);
-      if (j >= J || tile0 + j < Tw || k >= n) return -1;
-      return P.topk_idx != nullptr ? sm.list[k] : pool_row(k);
-    };
-    int next_row = fetch(done);
-    for (int j = done; j < J; ++j) {
+    int next_entry = entry_of(1), next_row = pool_row(entry_of(0));
+    for (int j = 0; j < J; ++j) {
       const int stage = j & (kStages8 - 1);
+      const int my_row = next_row;
+      next_row = pool_row(next_entry);
+      next_entry = entry_of(j + 2);
       if (j >= kStages8) {
         if (!mbar_wait(&sm.kv_free[stage], (uint32_t)((j / kStages8 - 1) & 1), abort_flag, status, 302)) break;
       } else if (j >= 2) {
         if (!mbar_wait(&sm.q_done, 0, abort_flag, status, 301)) break;
       }
-      const int my_row = next_row;
-      next_row = fetch(j + 1);
-      if (tile0 + j < Tw) {
-        window_tile(tile0 + j, stage);
+      bool win;
+      const int index = tile_of(tile0 + j, Tw, Te, win);
+      if (win) {
+        window_store(index, stage);
         continue;
       }
       const uint32_t st = smem_u32(stages + (size_t)stage * kStage) + (uint32_t)(lane >> 3) * kBlk;
@@ -358,60 +413,68 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
     }
     cp_async_wait_all();  // after an abort: let the copies land before teardown
     if (bad && half == 0) record_status(status, CSA_DEV_BOUNDS);
-  } else if (warp < kPvWarp8) {
-    // ------------------------------------------------------------ score MMAs: tiles j = w, w + 2, ...
-    if (lane == 0) {
-      const int w = warp - kQkWarp;
-      const bool ok = mbar_wait(&sm.q_done, 0, abort_flag, status, 311) &&
-                      mbar_wait(&sm.list_ready, 0, abort_flag, status, 312);
-      const int J = ok ? sm.n_tiles : 0;
-      const uint32_t idesc1 = idesc_fp8_f32(kE4M3, kE4M3, 128, kRows, 0, 0);
-      const uint32_t idesc2 = idesc_fp8_f32(kE5M2, kE4M3, 128, kRows, 0, 0);
-      const uint32_t qa = smem_u32(q2), d_s = tmem + 128 + kRows * w;
-      for (int j = w; j < J; j += 2) {
-        const int stage = j & (kStages8 - 1);
-        if (j >= 2 && !mbar_wait(&sm.s_free[w], (uint32_t)((j / 2 - 1) & 1), abort_flag, status, 313)) break;
-        if (!mbar_wait(&sm.kv_full[stage], (uint32_t)((j / kStages8) & 1), abort_flag, status, 314)) break;
-        fence_proxy_async_smem();  // rows written by cp.async before the MMAs read them
-        tc_fence_after();
-        const uint32_t kb = smem_u32(stages + (size_t)stage * kStage);
+  } else if (warp == kQkWarp) {
+    // ------------------------------------------------------------ score MMAs
+    // The whole warp walks the loop, so that addresses and descriptors stay in uniform registers (a thread by
+    // itself in a divergent branch took 80 cycles to issue each MMA of 47); one thread issues.
+    const bool leader = elect_one();
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_done, 0, abort_flag, status, 311)) &&
+                    __all_sync(0xffffffffu, mbar_wait(&sm.list_ready, 0, abort_flag, status, 312));
+    const int J = ok ? sm.n_tiles : 0;
+    constexpr uint32_t idesc1 = idesc_fp8_f32(kE4M3, kE4M3, 128, kRows, 0, 0);
+    constexpr uint32_t idesc2 = idesc_fp8_f32(kE5M2, kE4M3, 128, kRows, 0, 0);
+    const uint64_t dk = smem_desc_sw128(smem_u32(stages), 16, 1024), dq = smem_desc_sw128(smem_u32(q2), 16, 1024);
+    for (int j = 0; j < J; ++j) {
+      const int stage = j & (kStages8 - 1);
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[stage], (uint32_t)((j / kStages8) & 1), abort_flag, status, 314))) break;
+      if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.s_free, (uint32_t)((j - 1) & 1), abort_flag, status, 313))) break;
+      fence_proxy_async_smem();  // rows written by cp.async before the MMAs read them
+      tc_fence_after();
+      const uint64_t db = dk + (uint64_t)((uint32_t)stage * (kStage >> 4));
+      if (leader) {
 #pragma unroll
         for (int ks = 0; ks < 16; ++ks)
-          mma8_ts(d_s, tmem + 8 * ks, smem_desc_sw128(kb + (ks >> 2) * kBlk + (ks & 3) * 32, 16, 1024), idesc1,
-                  ks > 0 ? 1u : 0u);
+          mma8_ts(tmem + kScoreCol, tmem + 8 * ks, db + (((ks >> 2) * kBlk + (ks & 3) * 32) >> 4), idesc1, ks > 0 ? 1u : 0u);
 #pragma unroll
         for (int ks = 0; ks < 16; ++ks)
-          mma8_ss(d_s, smem_desc_sw128(qa + (ks >> 2) * kQBlk + (ks & 3) * 32, 16, 1024),
-                  smem_desc_sw128(kb + (ks >> 2) * kBlk + (ks & 3) * 32, 16, 1024), idesc2, 1u);
-        mma_commit(&sm.s_full[w]);
+          mma8_ss(tmem + kScoreCol, dq + (((ks >> 2) * kQBlk + (ks & 3) * 32) >> 4),
+                  db + (((ks >> 2) * kBlk + (ks & 3) * 32) >> 4), idesc2, 1u);
+        mma_commit(&sm.s_full[j & 1]);
       }
-      // Every MMA issued above completes on its own; wait for them before TMEM is released.
-      mma_commit(&sm.drain[w]);
-      mbar_wait_drain(&sm.drain[w], 0, status, 315);
+      __syncwarp();
+    }
+    // Every MMA issued above completes on its own; wait for them before TMEM is released.
+    if (leader) {
+      mma_commit(&sm.drain[0]);
+      mbar_wait_drain(&sm.drain[0], 0, status, 315);
     }
   } else if (warp == kPvWarp8) {
-    // ------------------------------------------------------------ PV MMAs, in tile order
-    if (lane == 0) {
-      const int J = mbar_wait(&sm.list_ready, 0, abort_flag, status, 321) ? sm.n_tiles : 0;
-      const uint32_t idesc[2] = {idesc_fp8_f32(kE4M3, kE4M3, 128, 256, 0, 1), idesc_fp8_f32(kE5M2, kE4M3, 128, 256, 0, 1)};
-      for (int j = 0; j < J; ++j) {
-        const int stage = j & (kStages8 - 1), g = j & 1;
-        if (!mbar_wait(&sm.p_full[g], (uint32_t)((j / 2) & 1), abort_flag, status, 322)) break;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint32_t vb = smem_u32(stages + (size_t)stage * kStage) + (uint32_t)half * 2 * kBlk;
-        const uint32_t pc = tmem + 128 + kRows * g;
+    // ------------------------------------------------------------ PV MMAs
+    const bool leader = elect_one();
+    const int J = __all_sync(0xffffffffu, mbar_wait(&sm.list_ready, 0, abort_flag, status, 321)) ? sm.n_tiles : 0;
+    constexpr uint32_t idesc[2] = {idesc_fp8_f32(kE4M3, kE4M3, 128, 256, 0, 1), idesc_fp8_f32(kE5M2, kE4M3, 128, 256, 0, 1)};
+    const uint64_t dv = smem_desc_sw128(smem_u32(stages) + (uint32_t)half * 2 * kBlk, kBlk, 1024);
+    for (int j = 0; j < J; ++j) {
+      const int stage = j & (kStages8 - 1), g = j & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.p_full[g], (uint32_t)((j / 2) & 1), abort_flag, status, 322))) break;
+      fence_proxy_async_smem();
+      tc_fence_after();
+      const uint64_t db = dv + (uint64_t)((uint32_t)stage * (kStage >> 4));
+      if (leader) {
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks)
-            mma8_ts(tmem + 256, pc + 16 * part + 8 * ks, smem_desc_sw128(vb + ks * 4096, kBlk, 1024), idesc[part],
+            mma8_ts(tmem + kOCol, tmem + kPCol + 32 * g + 16 * part + 8 * ks, db + ((ks * 4096) >> 4), idesc[part],
                     (j > 0 || part > 0 || ks > 0) ? 1u : 0u);
         mma_commit(&sm.kv_free[stage]);
-        mma_commit(&sm.s_free[g]);
+        mma_commit(&sm.pv_done[j & 3]);
       }
-      mma_commit(&sm.drain[2]);
-      mbar_wait_drain(&sm.drain[2], 0, status, 323);
+      __syncwarp();
+    }
+    if (leader) {
+      mma_commit(&sm.drain[1]);
+      mbar_wait_drain(&sm.drain[1], 0, status, 323);
     }
   } else {
     // ------------------------------------------------------------ q split, softmax, epilogue
@@ -420,37 +483,30 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
     const int quad = warp & 3;                 // TMEM lane quadrant
     const int h = quad * 32 + lane;            // head = TMEM lane
     const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
-    // q rows 16 sw .. 16 sw + 15, eight in flight.
+    // q rows 16 sw .. 16 sw + 15, two at a time and three reads ahead.
+    {
+      RowPair w[3];
+      auto q_read = [&](RowPair& r2, int r) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          read_row(r2, i, P.q + ((long long)qi * P.H + (r + i)) * 512, r + i < P.H && r < 16 * sw + 16);
+      };
+#pragma unroll
+      for (int i = 0; i < 3; ++i) q_read(w[i], 16 * sw + 2 * i);
 #pragma unroll 1
-    for (int r0 = 0; r0 < 16; r0 += 8) {
-      uint4 a[8], c[8];
+      for (int r = 16 * sw; r < 16 * sw + 16; r += 2) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 16 * sw + r0 + i;
-        a[i] = c[i] = make_uint4(0, 0, 0, 0);
-        if (r < P.H) {
-          const uint4* src = reinterpret_cast<const uint4*>(P.q + ((long long)qi * P.H + r) * 512);
-          a[i] = src[lane];
-          c[i] = src[32 + lane];
+        for (int i = 0; i < 2; ++i) {
+          RowPieces pc;
+          const float f = split_row<true>(w[0].a[i], w[0].c[i], pc);
+          store_codes(q1s, kQBlk, r + i, lane, pc.hi);
+          store_codes(q2, kQBlk, r + i, lane, pc.lo);
+          if (lane == 0) sm.qf[r + i] = f * P.scale_log2;
         }
+        w[0] = w[1];
+        w[1] = w[2];
+        q_read(w[2], r + 6);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 16 * sw + r0 + i;
-        RowPieces pc;
-        const float f = split_row<true>(a[i], c[i], pc);
-        store_codes(q1s, kQBlk, r, lane, pc.hi);
-        store_codes(q2, kQBlk, r, lane, pc.lo);
-        if (lane == 0) sm.qf[r] = f * P.scale_log2;
-      }
-    }
-    // Inverse-RoPE table for position t.
-    const int st = threadIdx.x - kSoftWarp * 32;  // 0..255
-    if (st < P.rope_dim / 2) {
-      float cs, sn;
-      rope_cos_sin(t, P.inv_freq[st], &cs, &sn);
-      sm.rope_cs[st][0] = cs;
-      sm.rope_cs[st][1] = -sn;
     }
     fence_proxy_async_smem();  // q2 before the MMAs read it
     named_bar_sync(1, 2 * kGroup);
@@ -472,20 +528,30 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
     tc_fence_before();
     mbar_arrive(&sm.q_done);
 
+    // Inverse-RoPE table for position t, while the first scores are on their way (the epilogue's barrier orders it).
+    const int st = threadIdx.x - kSoftWarp * 32;  // 0..255
+    if (st < P.rope_dim / 2) {
+      float cs, sn;
+      rope_cos_sin(t, P.inv_freq[st], &cs, &sn);
+      sm.rope_cs[st][0] = cs;
+      sm.rope_cs[st][1] = -sn;
+    }
     bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.list_ready, 0, abort_flag, status, 331));
     const int J = ok ? sm.n_tiles : 0;
-    const int tile0 = sm.tile0;
+    const int tile0 = sm.tile0, Te = sm.entry_tiles;
     const float qf = sm.qf[h];
-    // s_free[i % 2] completes once per PV(i). A wait for PV(i) by parity is unambiguous while PV(i - 2) is
-    // known to have completed and PV(i + 2) cannot have: scores of tile j exist only after PV(j - 2), and
-    // PV(j + 1) needs the maximum that the group of tile j has not yet published.
+    const uint64_t qf2 = pack2(qf, qf);
+    // pv_done[i % 4] completes once per PV(i). A wait for PV(i) by parity is unambiguous while PV(i - 4) is known to have
+    // completed and PV(i + 4) cannot have. A group waits for PV(j - 2) before it stores P(j), and publishes its maximum of
+    // tile j after that of tile j - 2: so whoever holds the maximum of tile j - 1 knows that PV(j - 5) completed.
     auto wait_pv = [&](int i) -> bool {
-      return i < 0 || __all_sync(0xffffffffu, mbar_wait(&sm.s_free[i & 1], (uint32_t)((i / 2) & 1), abort_flag, status, 332));
+      return i < 0 || __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[i & 3], (uint32_t)((i / 4) & 1), abort_flag, status, 332));
     };
     float m_used = -CUDART_INF_F, l = 0.f;
     for (int j = g; j < J; j += 2) {
       const int stage = j & (kStages8 - 1);
-      const bool win = tile0 + j < Tw;
+      bool win;
+      tile_of(tile0 + j, Tw, Te, win);
       // Column factors, two columns a lane, while the score MMAs run. A window candidate's second column
       // adds nothing to the denominator.
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[stage], (uint32_t)((j / kStages8) & 1), abort_flag, status, 333))) {
@@ -507,37 +573,38 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
         break;
       }
       tc_fence_after();
-      const uint32_t s_addr = tmem + lane_addr + 128 + kRows * g;
-      float y[kRows];
+      uint64_t y[kRows / 2];
       {
         uint32_t v0[32], v1[32];
-        tmem_ld32(s_addr, v0);
-        tmem_ld32(s_addr + 32, v1);
+        tmem_ld32(tmem + lane_addr + kScoreCol, v0);
+        tmem_ld32(tmem + lane_addr + kScoreCol + 32, v1);
         tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(&sm.s_free);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          y[c] = pack2(__uint_as_float(v0[2 * c]), __uint_as_float(v0[2 * c + 1]));
+          y[c + 16] = pack2(__uint_as_float(v1[2 * c]), __uint_as_float(v1[2 * c + 1]));
+        }
         if (win) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) y[c] = y[c + 32] = __uint_as_float(v0[c]) + __uint_as_float(v1[c]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            y[c] = __uint_as_float(v0[c]);
-            y[c + 32] = __uint_as_float(v1[c]);
-          }
+          for (int c = 0; c < 16; ++c) y[c] = y[c + 16] = add2(y[c], y[c + 16]);
         }
       }
-      float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+      float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-      for (int c = 0; c < kRows; c += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(&sm.col_a[sw][c]);
-        const float4 k = *reinterpret_cast<const float4*>(&sm.col_k[sw][c]);
-        y[c] = fmaf(y[c] * qf, a.x, k.x);
-        y[c + 1] = fmaf(y[c + 1] * qf, a.y, k.y);
-        y[c + 2] = fmaf(y[c + 2] * qf, a.z, k.z);
-        y[c + 3] = fmaf(y[c + 3] * qf, a.w, k.w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], y[c + e]);
+      for (int c = 0; c < kRows / 2; c += 2) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&sm.col_a[sw][2 * c]);
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sm.col_k[sw][2 * c]);
+        y[c] = fma2(mul2(y[c], qf2), a.x, k.x);
+        y[c + 1] = fma2(mul2(y[c + 1], qf2), a.y, k.y);
+        float e0, e1, e2, e3;
+        unpack2(y[c], e0, e1);
+        unpack2(y[c + 1], e2, e3);
+        mx[0] = fmaxf(mx[0], fmaxf(e0, e1));
+        mx[1] = fmaxf(mx[1], fmaxf(e2, e3));
       }
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const float mt = fmaxf(mx[0], mx[1]);
       // The running maximum after tile j - 1, from the other group (it only grows).
       if (j > 0) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.hand[1 - g][quad], (uint32_t)(((j - 1) / 2) & 1), abort_flag, status, 335))) {
@@ -551,7 +618,7 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
         }
       }
       // Lazy rescale; the TMEM accesses are warp-collective, so the warp takes the branch if any lane must.
-      const bool need = mt > m_used + kHead || (m_used == -CUDART_INF_F && mt > m_used);
+      const bool need = mt > m_used + (kHead + kOver) || (m_used == -CUDART_INF_F && mt > m_used);
       if (__any_sync(0xffffffffu, need)) {
         const float alpha = need ? exp2f(m_used - mt) : 1.f;
         if (j > 0) {
@@ -560,15 +627,21 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
             break;
           }
           tc_fence_after();
+          const uint64_t alpha2 = pack2(alpha, alpha);
 #pragma unroll 1
-          for (int cc = 0; cc < 16; ++cc) {
-            uint32_t o[16];
-            const uint32_t oa = tmem + lane_addr + 256 + 16 * cc;
-            tmem_ld16(oa, o);
+          for (int cc = 0; cc < 8; ++cc) {
+            uint32_t o[32];
+            const uint32_t oa = tmem + lane_addr + kOCol + 32 * cc;
+            tmem_ld32(oa, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st16(oa, o);
+            for (int e = 0; e < 32; e += 2) {
+              float a0, a1;
+              unpack2(mul2(pack2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), alpha2), a0, a1);
+              o[e] = __float_as_uint(a0);
+              o[e + 1] = __float_as_uint(a1);
+            }
+            tmem_st32(oa, o);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -583,29 +656,42 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
         mbar_arrive(&sm.hand[g][quad]);
       }
       const float ref = (m_used == -CUDART_INF_F ? 0.f : m_used) + kHead;
+      const uint64_t ref2 = pack2(-ref, -ref);
       uint32_t p1[16], p2[16];
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t ls[2] = {0, 0};
 #pragma unroll
-      for (int c = 0; c < kRows; c += 4) {
-        const float4 ki = *reinterpret_cast<const float4*>(&sm.col_i[sw][c]);
-        float p[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(y[c + e] - ref);
-        ls[0] = fmaf(p[0], ki.x, ls[0]);
-        ls[1] = fmaf(p[1], ki.y, ls[1]);
-        ls[2] = fmaf(p[2], ki.z, ls[2]);
-        ls[3] = fmaf(p[3], ki.w, ls[3]);
-        split_p(p, p1[c / 4], p2[c / 4]);
+      for (int c = 0; c < kRows / 2; c += 2) {
+        const ulonglong2 ki = *reinterpret_cast<const ulonglong2*>(&sm.col_i[sw][2 * c]);
+        float e0, e1, e2, e3;
+        unpack2(add2(y[c], ref2), e0, e1);
+        unpack2(add2(y[c + 1], ref2), e2, e3);
+        e0 = ex2_approx(e0);
+        e1 = ex2_approx(e1);
+        e2 = ex2_approx(e2);
+        e3 = ex2_approx(e3);
+        ls[0] = fma2(pack2(e0, e1), ki.x, ls[0]);
+        ls[1] = fma2(pack2(e2, e3), ki.y, ls[1]);
+        split_p(e0, e1, e2, e3, p1[c / 2], p2[c / 2]);
       }
-      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-      tmem_st16(s_addr, p1);
-      tmem_st16(s_addr + 16, p2);
+      {
+        float s0, s1;
+        unpack2(add2(ls[0], ls[1]), s0, s1);
+        l += s0 + s1;
+      }
+      if (!wait_pv(j - 2)) {  // the P buffer is free
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t pa = tmem + lane_addr + kPCol + 32 * g;
+      tmem_st16(pa, p1);
+      tmem_st16(pa + 16, p2);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&sm.p_full[g]);
     }
-    // Every PV completed. PV(J - 2) first: only then is the parity of PV(J - 1) unambiguous.
-    if (ok && J > 0 && (!wait_pv(J - 2) || !wait_pv(J - 1))) ok = false;
+    // Every PV completed.
+    if (ok && J > 0 && (!wait_pv(J - 5) || !wait_pv(J - 2) || !wait_pv(J - 1))) ok = false;
     sm.l_g[g][h] = l;
     sm.m_g[g][h] = m_used;
     if (!ok && lane == 0) sm.epi_bad = 1;
@@ -647,12 +733,16 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
     const bool read_o = J > 0 && any;
     if (fin) {
       const int rope0 = 512 - P.rope_dim;
-      uint8_t* srow = stages + (size_t)h * kRowPitch;  // every gather and MMA that reads the stages completed
+      // Rows are staged in shared memory (the stages, then q2's place: every gather and MMA completed), 16 bytes apart
+      // against bank conflicts, and leave whole.
+      const bool wide = P.splits > 1 || P.out_is_f32;
+      const uint32_t row_bytes = wide ? 1024 : 512;
+      uint8_t* srow = stages + (size_t)h * (row_bytes + 16);
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         const int lc = 128 * g + 32 * cc, col0 = 256 * half + lc;
         uint32_t o[32];
-        tmem_ld32(tmem + lane_addr + 256 + lc, o);
+        tmem_ld32(tmem + lane_addr + kOCol + lc, o);
         tmem_wait_ld();
         float v[32];
 #pragma unroll
@@ -669,14 +759,10 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
             }
           }
         }
-        if (P.splits > 1 || P.out_is_f32) {
-          if (h < P.H) {
-            float* dst = P.splits > 1 ? P.part_o + ((long long)item * P.H + h) * 512 + col0
-                                      : static_cast<float*>(P.out) + ((long long)qi * P.H + h) * 512 + col0;
+        if (wide) {
+          float4* dst = reinterpret_cast<float4*>(srow + 4 * lc);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              reinterpret_cast<float4*>(dst)[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-          }
+          for (int c = 0; c < 8; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
         } else {
           uint4* dst = reinterpret_cast<uint4*>(srow + 2 * lc);
 #pragma unroll
@@ -685,15 +771,17 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
                                 pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
         }
       }
-      if (P.splits == 1 && !P.out_is_f32) {
-        // Each head row's 512 bytes leave in one bulk store, once both groups staged their halves.
-        fence_proxy_async_smem();
-        named_bar_sync(1, 2 * kGroup);
-        if (g == 0 && h < P.H) {
-          bulk_store_global(static_cast<uint16_t*>(P.out) + ((long long)qi * P.H + h) * 512 + 256 * half, smem_u32(srow), 512);
-          bulk_commit();
-          bulk_wait_read_all();
-        }
+      // Each head row's bytes leave in one bulk store, once both groups staged their halves.
+      fence_proxy_async_smem();
+      named_bar_sync(1, 2 * kGroup);
+      if (g == 0 && h < P.H) {
+        const long long at = ((long long)(P.splits > 1 ? item : qi) * P.H + h) * 512 + 256 * half;
+        void* dst = P.splits > 1 ? static_cast<void*>(P.part_o + at)
+                    : P.out_is_f32 ? static_cast<void*>(static_cast<float*>(P.out) + at)
+                                   : static_cast<void*>(static_cast<uint16_t*>(P.out) + at);
+        bulk_store_global(dst, smem_u32(srow), row_bytes);
+        bulk_commit();
+        bulk_wait_read_all();
       }
     }
   }

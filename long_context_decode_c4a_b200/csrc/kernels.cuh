@@ -176,7 +176,7 @@ __global__ void attn_combine_kernel(AttnCombineParams P);
 
 // ------------------------------------------------------------------------------ attention over 8-bit pages
 
-constexpr int kAttn8Threads = 480;        // warps 0..3 gathers, 4-5 score MMAs, 6 PV MMAs, 7..14 softmax
+constexpr int kAttn8Threads = 448;        // warps 0..3 gathers, 4 score MMAs, 5 PV MMAs, 6..13 softmax
 
 struct Attn8Params {
   int B, S, H, rope_dim;

@@ -54,7 +54,8 @@ def make_q(g, *shape):
 def reference(q, t, W, ring, cache, scales, selected, sink, scale, rope_dim, rope_base):
     """The oracle's output of one query, how far the kernel may be from it, from the roundings that it makes, and the mean of
     sum (w c)^2 over the output:
-      a weight P is off by 2^-8 of itself or 2^-22 of the largest P (P holds the scale of its column);
+      a weight P is off by 2^-8 of itself, or where that is less by 2^-22 with the largest P (P holds the scale of its column) at
+      2^-5 or more, and by 2^-4 of itself or 2^-25 at most;
       a score by 2^-21 max|q| sum|c| (q's second piece), 2^-17 max|c| sum|q| (a window row's), 1024 additions
       of fp32 (2^-23 each) and the rounding of the exponent's argument;
       O by its additions in fp32 (2^-23 each), a window value by 2^-17 of its row's largest.
@@ -77,8 +78,10 @@ def reference(q, t, W, ring, cache, scales, selected, sink, scale, rope_dim, rop
         dl = abs(scale) * (2.0 ** -13 * aq @ ac.T + 2.0 ** -21 * aq.max(1)[:, None] * ac.sum(1))
         dl[:, :nw] += abs(scale) * 2.0 ** -17 * ac[:nw].max(1, initial=0) * aq.sum(1)[:, None]
         dl += 2.0 ** -22 * (np.abs(l) + np.abs(m)[:, None] + 32) + 2.0 ** -21
-        rel = 2.0 ** -8 + n * 2.0 ** -23 + dl + (w * dl).sum(1, keepdims=True)
-        tol = (w * rel) @ ac + 2.0 ** -22 * (w * s).max(1)[:, None] * (ac / np.where(s == 0, 1, s)[:, None]).sum(0)
+        rel = n * 2.0 ** -23 + dl + (w * dl).sum(1, keepdims=True)
+        p, codes = w * s, ac / np.where(s == 0, 1, s)[:, None]
+        unit = p.max(1, keepdims=True) * 2.0 ** 5
+        tol = (w * rel) @ ac + np.maximum(2.0 ** -8 * p, np.minimum(2.0 ** -22 * unit, 2.0 ** -4 * p + 2.0 ** -25 * unit)) @ codes
         tol += (w[:, :nw] * 2.0 ** -17) @ np.repeat(ac[:nw].max(1, initial=0)[:, None], D, 1)
     r0 = D - rope_dim
     pair = tol[:, r0:].reshape(len(q), -1, 2).sum(-1, keepdims=True).repeat(2, -1).reshape(len(q), -1)

@@ -487,27 +487,38 @@ CSA_API int csa_indexer_topk_paged(const csa_page_table* pt, const csa_paged_cac
                                    int ratio, int topk, const int32_t* q_pos, const uint16_t* q_idx, const float* w,
                                    int32_t* topk_idx, float* scores_opt, void* ws, size_t ws_bytes, void* stream);
 
+/* Arguments of csa_sparse_attn8 and hca_attn8. */
+typedef struct {
+  const csa_page_table* pt;
+  const csa_paged_cache* cache;  /* 8 bits */
+  const int32_t* q_pos;          /* dev [B, S]; negative: a padding query */
+  const uint16_t* q;             /* dev bf16 [B, S, H, 512] */
+  const uint16_t* ring;          /* dev bf16, slot j of request b at ring + b*ring_bstride + j*512 */
+  const int32_t* topk_idx;       /* dev [B, S, topk], -1: none (hca_attn8: not looked at) */
+  const float* sink;             /* dev [H] */
+  void* out;                     /* dev [B, S, H, 512]: bf16, or float if out_is_f32 */
+  void* ws;
+  size_t ws_bytes;
+  int64_t ring_bstride;          /* a multiple of 8, >= ring_cap * 512 */
+  int B, S, H, rope_dim;
+  float rope_base, scale;
+  int ratio, ring_cap, window, topk, out_is_f32;
+} csa_attn8_args;
+
 /*
  * csa_sparse_attn8 / hca_attn8 -- csa_sparse_attn / hca_attn over an 8-bit cache in pages: the entries count with
- * their dequantised values, the window rows stay bf16. csa_sparse_attn8 takes the entries of topk_idx (-1: none); hca_attn8
- * every entry s < (t+1)/ratio, any number of them. A negative q_pos marks a padding query: its output is zero. A query
- * with no candidate has output zero too.
- *   ring, q, sink, out, rope and scale as in csa_sparse_attn; d = 512, 1 <= H <= 128, rope_dim even and <= 128,
- *   window in [1, 1024], topk in [1, 2048]; ring_bstride a multiple of 8; ring_cap >= window + S - 1 for the
- *   rows of a segment's queries to be all there (the caller's choice, not checked).
- *   ws: csa_workspace_size(CSA_WS_SPARSE_ATTN, ...) / CSA_WS_HCA_ATTN, or only its status word (slower for few queries).
+ * their dequantised values, the window rows stay bf16. csa_sparse_attn8 takes the entries of topk_idx; hca_attn8
+ * every entry s < (t+1)/ratio, any number of them. The output of a padding query is zero, and so is that of a
+ * query with no candidate.
+ *   1 <= H <= 128; rope_dim even and <= 128; window in [1, 1024], <= ring_cap; topk in [1, 2048]. The rows of a
+ *   segment's queries are all there if ring_cap >= window + S - 1 (the caller's choice, not checked).
+ *   Pointers 16-byte aligned. ws: csa_workspace_size(CSA_WS_SPARSE_ATTN, ...) / CSA_WS_HCA_ATTN, or only its
+ *   status word (slower for few queries).
  * A selected entry that is not visible at t, a visible one (range form) beyond the table, or an entry whose page is
  * not mapped is skipped and records CSA_ERR_BOUNDS.
  */
-CSA_API int csa_sparse_attn8(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int H, int rope_dim,
-                             float rope_base, float scale, int ratio, const int32_t* q_pos, const uint16_t* q,
-                             const uint16_t* ring, int64_t ring_bstride, int ring_cap, int window,
-                             const int32_t* topk_idx, int topk, const float* sink, void* out, int out_is_f32, void* ws,
-                             size_t ws_bytes, void* stream);
-CSA_API int hca_attn8(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int H, int rope_dim,
-                      float rope_base, float scale, int ratio, const int32_t* q_pos, const uint16_t* q,
-                      const uint16_t* ring, int64_t ring_bstride, int ring_cap, int window, const float* sink,
-                      void* out, int out_is_f32, void* ws, size_t ws_bytes, void* stream);
+CSA_API int csa_sparse_attn8(const csa_attn8_args* a, void* stream);
+CSA_API int hca_attn8(const csa_attn8_args* a, void* stream);
 
 /*
  * csa_get_device_status -- synchronise `stream`, read the status word in `ws` into *status

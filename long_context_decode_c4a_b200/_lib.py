@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import POINTER, c_char_p, c_float, c_int, c_int64, c_size_t, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -79,6 +80,18 @@ class PagedCacheArg(ctypes.Structure):
     _fields_ = [("d", c_int), ("block", c_int), ("pages", c_void_p), ("scales", c_void_p)]
 
 
+class Attn8Args(ctypes.Structure):
+    """Mirror of csa_attn8_args."""
+    _fields_ = [("pt", c_void_p), ("cache", c_void_p), ("q_pos", c_void_p), ("q", c_void_p), ("ring", c_void_p),
+                ("topk_idx", c_void_p), ("sink", c_void_p), ("out", c_void_p), ("ws", c_void_p), ("ws_bytes", c_size_t),
+                ("ring_bstride", c_int64), ("B", c_int), ("S", c_int), ("H", c_int), ("rope_dim", c_int),
+                ("rope_base", c_float), ("scale", c_float), ("ratio", c_int), ("ring_cap", c_int), ("window", c_int),
+                ("topk", c_int), ("out_is_f32", c_int)]
+
+
+# The same, packed in one go (a ctypes call converts one argument after another: 6 us for this many).
+pack_attn8 = struct.Struct("9PNq4i2f5i0P").pack
+
 _PT, _PC = POINTER(PageTableArg), POINTER(PagedCacheArg)
 
 # name -> (restype, argtypes)
@@ -126,11 +139,8 @@ PROTOTYPES = {
                                          c_void_p, c_size_t, c_void_p]),
     "csa_indexer_topk_paged": (c_int, [_PT, _PC, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,
                                        c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
-    "csa_sparse_attn8": (c_int, [_PT, _PC, c_int, c_int, c_int, c_int, c_float, c_float, c_int, c_void_p, c_void_p,
-                                 c_void_p, c_int64, c_int, c_int, c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p,
-                                 c_size_t, c_void_p]),
-    "hca_attn8": (c_int, [_PT, _PC, c_int, c_int, c_int, c_int, c_float, c_float, c_int, c_void_p, c_void_p, c_void_p,
-                          c_int64, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "csa_sparse_attn8": (c_int, [c_void_p, c_void_p]),
+    "hca_attn8": (c_int, [c_void_p, c_void_p]),
 }
 
 _lib = None

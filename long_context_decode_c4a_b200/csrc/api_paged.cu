@@ -38,7 +38,7 @@ int check_cache(const csa_page_table* pt, const csa_paged_cache* c) {
 }
 
 struct PagesWs {
-  size_t counts, n_moves, list_a, list_b, move_src, move_dst, heir, rows, total;
+  size_t counts, n_moves, list_a, list_b, move_src, move_dst, heir, need, copy, rows, total;
 };
 
 PagesWs pages_ws_layout(long long slots, long long max_pages, long long num_pages) {
@@ -56,6 +56,8 @@ PagesWs pages_ws_layout(long long slots, long long max_pages, long long num_page
   w.move_src = take(num_pages);
   w.move_dst = take(num_pages);
   w.heir = take(slots);
+  w.need = take(slots);
+  w.copy = take(slots);
   w.rows = take(slots * max_pages);
   w.total = off;
   return w;
@@ -79,9 +81,16 @@ int pages_params(const csa_page_table* pt, void* ws, size_t ws_bytes, PagesParam
   P->move_src = reinterpret_cast<int*>(base + w.move_src);
   P->move_dst = reinterpret_cast<int*>(base + w.move_dst);
   P->heir = reinterpret_cast<int*>(base + w.heir);
+  P->need = reinterpret_cast<int*>(base + w.need);
+  P->copy = reinterpret_cast<int*>(base + w.copy);
   P->rows = reinterpret_cast<int*>(base + w.rows);
   P->status = reinterpret_cast<uint32_t*>(ws);
   return CSA_OK;
+}
+
+cudaError_t launch_table(void (*one)(PagesParams), void (*cluster)(PagesParams), const PagesParams& P, cudaStream_t st) {
+  const bool small = (long long)P.slots * P.max_pages + P.num_pages <= kPagesSmall && P.slots <= kPagesSmallSlots;
+  return launch_pdl(small ? one : cluster, dim3(small ? 1 : kPagesCluster), dim3(kPagesThreads), 0, st, P);
 }
 
 int check_caches(const csa_page_table* pt, const csa_paged_cache* caches, int n) {
@@ -120,24 +129,11 @@ int copy_pages(const csa_page_table* pt, const csa_paged_cache* caches, int n, l
   return CSA_OK;
 }
 
-struct Attn8Args {
-  int B, S, H, rope_dim;
-  float rope_base, scale;
-  int ratio;
-  const int32_t* q_pos;
-  const uint16_t *q, *ring;
-  int64_t ring_bstride;
-  int ring_cap, window;
-  const int32_t* topk_idx;
-  int topk;
-  const float* sink;
-  void* out;
-  int out_is_f32;
-  void* ws;
-  size_t ws_bytes;
-};
-
-int run_attn8(const csa_page_table* pt, const csa_paged_cache* c, const Attn8Args& a, bool list, cudaStream_t st) {
+int run_attn8(const csa_attn8_args* args, bool list, cudaStream_t st) {
+  CSA_CHECK_ARG(args != nullptr, "args is null");
+  const csa_attn8_args& a = *args;
+  const csa_page_table* pt = a.pt;
+  const csa_paged_cache* c = a.cache;
   if (int rc = check_paged(pt, c, a.B, true)) return rc;
   CSA_CHECK_ARG(a.S > 0, "S must be positive");
   CSA_CHECK_SUP(a.H >= 1 && a.H <= 128, "H must be in [1, 128]");
@@ -165,7 +161,9 @@ int run_attn8(const csa_page_table* pt, const csa_paged_cache* c, const Attn8Arg
   P.S = a.S;
   P.H = a.H;
   P.rope_dim = a.rope_dim;
-  for (int i = 0; i < a.rope_dim / 2; ++i) P.inv_freq[i] = std::pow((double)a.rope_base, -2.0 * i / a.rope_dim);
+  const double step = std::pow((double)a.rope_base, -2.0 / a.rope_dim);
+  P.inv_freq[0] = 1.0;
+  for (int i = 1; i < a.rope_dim / 2; ++i) P.inv_freq[i] = P.inv_freq[i - 1] * step;
   P.scale_log2 = a.scale * 1.4426950408889634f;
   P.window = a.window;
   P.ring_cap = a.ring_cap;
@@ -319,7 +317,7 @@ int csa_pages_reserve(const csa_page_table* pt, const int32_t* entries, void* ws
   DeviceInfo* dev;
   if (int rc = device_info(&dev)) return rc;
   P.entries = entries;
-  CSA_CUDA(launch_pdl(pages_reserve_kernel, dim3(kPagesCluster), dim3(kPagesThreads), 0, static_cast<cudaStream_t>(stream), P));
+  CSA_CUDA(launch_table(pages_reserve_kernel, pages_reserve_cluster_kernel, P, static_cast<cudaStream_t>(stream)));
   return CSA_OK;
 }
 
@@ -335,7 +333,7 @@ int csa_pages_fork(const csa_page_table* pt, const csa_paged_cache* caches, int 
   P.parent = parent;
   P.entries = entries;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  CSA_CUDA(launch_pdl(pages_fork_kernel, dim3(kPagesCluster), dim3(kPagesThreads), 0, st, P));
+  CSA_CUDA(launch_table(pages_fork_kernel, pages_fork_cluster_kernel, P, st));
   return copy_pages(pt, caches, n_caches, std::min(pt->slots, pt->num_pages), P, *dev, st);
 }
 
@@ -351,26 +349,12 @@ int csa_pages_compact(const csa_page_table* pt, const csa_paged_cache* caches, i
   P.map = map;
   P.live = live;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  CSA_CUDA(launch_pdl(pages_compact_kernel, dim3(kPagesCluster), dim3(kPagesThreads), 0, st, P));
+  CSA_CUDA(launch_table(pages_compact_kernel, pages_compact_cluster_kernel, P, st));
   return copy_pages(pt, caches, n_caches, pt->num_pages / 2 + 1, P, *dev, st);
 }
 
-int csa_sparse_attn8(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int H, int rope_dim,
-                     float rope_base, float scale, int ratio, const int32_t* q_pos, const uint16_t* q,
-                     const uint16_t* ring, int64_t ring_bstride, int ring_cap, int window, const int32_t* topk_idx,
-                     int topk, const float* sink, void* out, int out_is_f32, void* ws, size_t ws_bytes, void* stream) {
-  const Attn8Args a{B, S, H, rope_dim, rope_base, scale, ratio, q_pos, q, ring, ring_bstride, ring_cap, window,
-                    topk_idx, topk, sink, out, out_is_f32, ws, ws_bytes};
-  return run_attn8(pt, cache, a, true, static_cast<cudaStream_t>(stream));
-}
+int csa_sparse_attn8(const csa_attn8_args* a, void* stream) { return run_attn8(a, true, static_cast<cudaStream_t>(stream)); }
 
-int hca_attn8(const csa_page_table* pt, const csa_paged_cache* cache, int B, int S, int H, int rope_dim,
-              float rope_base, float scale, int ratio, const int32_t* q_pos, const uint16_t* q, const uint16_t* ring,
-              int64_t ring_bstride, int ring_cap, int window, const float* sink, void* out, int out_is_f32, void* ws,
-              size_t ws_bytes, void* stream) {
-  const Attn8Args a{B, S, H, rope_dim, rope_base, scale, ratio, q_pos, q, ring, ring_bstride, ring_cap, window,
-                    nullptr, 0, sink, out, out_is_f32, ws, ws_bytes};
-  return run_attn8(pt, cache, a, false, static_cast<cudaStream_t>(stream));
-}
+int hca_attn8(const csa_attn8_args* a, void* stream) { return run_attn8(a, false, static_cast<cudaStream_t>(stream)); }
 
 }  // extern "C"

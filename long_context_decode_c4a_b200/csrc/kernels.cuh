@@ -244,6 +244,8 @@ __global__ void cache_read_kernel(ReadParams P);
 
 constexpr int kPagesCluster = 8;          // CTAs of a page-table operation
 constexpr int kPagesThreads = 1024;
+constexpr int kPagesSmall = 8192;        // places + pages up to which one CTA does the work ...
+constexpr int kPagesSmallSlots = 2048;    // ... with at most this many slots (their arguments are in shared memory)
 
 struct PagesParams {
   int slots, max_pages, num_pages, page_shift;
@@ -261,6 +263,8 @@ struct PagesParams {
   int* move_src;                          // [num_pages]
   int* move_dst;
   int* heir;                              // [slots]
+  int* need;                              // [slots]
+  int* copy;                              // [slots]
   int* rows;                              // [slots, max_pages]
   uint32_t* status;
 };
@@ -268,6 +272,9 @@ struct PagesParams {
 __global__ void pages_reserve_kernel(PagesParams P);
 __global__ void pages_fork_kernel(PagesParams P);
 __global__ void pages_compact_kernel(PagesParams P);
+__global__ void pages_reserve_cluster_kernel(PagesParams P);
+__global__ void pages_fork_cluster_kernel(PagesParams P);
+__global__ void pages_compact_cluster_kernel(PagesParams P);
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;         // bytes a CTA copies at a time

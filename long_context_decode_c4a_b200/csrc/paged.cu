@@ -49,28 +49,49 @@ __device__ __forceinline__ int block_scan(int v, int* smem /* 33 ints */, int& t
   return r;
 }
 
-// Items [lo, hi) of [0, n) that this CTA of the cluster walks, and of those the run of this thread.
-__device__ __forceinline__ void my_run(long long n, long long& lo, long long& hi) {
-  const long long c = cluster_ctarank();
-  const long long a = n * c / kPagesCluster, b = n * (c + 1) / kPagesCluster;
-  const long long per = (b - a + blockDim.x - 1) / blockDim.x;
+// A page-table operation runs on C CTAs: a cluster of 8, or one CTA where the table is small (then barriers are the
+// CTA's, and the slots' arguments are in shared memory).
+template <int C>
+__device__ __forceinline__ void all_sync() {
+  if (C == 1) __syncthreads();
+  else cluster_sync();
+}
+template <int C>
+__device__ __forceinline__ unsigned rank() {
+  return C == 1 ? 0u : cluster_ctarank();
+}
+
+// Items [lo, hi) of [0, n) that this CTA walks, and of those the run of this thread.
+template <int C>
+__device__ __forceinline__ void my_run(unsigned n, unsigned& lo, unsigned& hi) {
+  const unsigned c = rank<C>(), each = (n + C - 1) / C;
+  const unsigned a = min(n, c * each), b = min(n, a + each);
+  const unsigned per = (b - a + blockDim.x - 1) / blockDim.x;
   lo = min(b, a + per * threadIdx.x);
   hi = min(b, lo + per);
 }
 
-// Sum of slot `what` of every earlier CTA of the cluster, and of all of them (each published its own before a
-// cluster barrier).
-__device__ __forceinline__ int cluster_prefix(const int* counts, int what, int& total) {
-  int before = 0;
-  total = 0;
-  const int c = (int)cluster_ctarank();
-#pragma unroll
-  for (int i = 0; i < kPagesCluster; ++i) {
-    const int v = ld_cg(counts + kPagesCluster * what + i);
-    before += i < c ? v : 0;
-    total += v;
+// Scan over all CTAs' threads: the sum of v in the threads before this one, and in all. Ends with a barrier of all, which also
+// orders what was written before it. `slot`: of P.counts, another for each scan.
+template <int C>
+__device__ __forceinline__ int all_scan(int v, int* smem, int* counts, int slot, int& total) {
+  int mine;
+  int r = block_scan(v, smem, mine);
+  if (C == 1) {
+    total = mine;
+    return r;
   }
-  return before;
+  const int c = (int)rank<C>();
+  if (threadIdx.x == 0) counts[C * slot + c] = mine;
+  all_sync<C>();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int x = ld_cg(counts + C * slot + i);
+    r += i < c ? x : 0;
+    total += x;
+  }
+  return r;
 }
 
 }  // namespace
@@ -265,66 +286,75 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(ReadParams P) 
 
 // ------------------------------------------------------------------------------------------------ page table
 //
-// The three table operations are integer scans over the table and the reference counts (a few hundred KB for
-// 64 requests at a million tokens): one cluster of 8 CTAs walks them, a contiguous run per thread, with
-// cluster barriers between the phases, so an operation on the table is one launch. What they cost is
-// latency: the barriers and dependent loads of each phase.
+// The three table operations are integer scans over the table and the reference counts (64 KB for 64 requests at
+// 32K, a few hundred at a million tokens) in one launch. What they cost is latency: the barriers and dependent loads of
+// each phase, so loads are issued four at a time. Up to kPagesSmall places and pages one CTA is quicker (its
+// barriers cost tens of nanoseconds); beyond, a cluster of 8. What depends on a slot alone is worked out first, by every CTA
+// in its own shared memory (S), or for more than kPagesSmallSlots slots once, in the workspace.
+
+// f(i, g(i)) for i = first, first + step, ... below n, with four g under way.
+template <typename G, typename F>
+__device__ __forceinline__ void batched(unsigned n, unsigned first, unsigned step, G g, F f) {
+  for (unsigned i = first; i < n; i += 4 * step) {
+    decltype(g(0u)) v[4];
+#pragma unroll
+    for (unsigned u = 0; u < 4; ++u)
+      if (i + u * step < n) v[u] = g(i + u * step);
+#pragma unroll
+    for (unsigned u = 0; u < 4; ++u)
+      if (i + u * step < n) f(i + u * step, v[u]);
+  }
+}
 
 // Pages for entries[r] entries of every slot: unmapped places below ceil(entries[r] / page_size), in (slot,
 // place) order, get the lowest free pages. With fewer free pages than places nothing changes.
-__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads) pages_reserve_kernel(PagesParams P) {
+template <int C, bool S>
+__device__ __forceinline__ void pages_reserve(const PagesParams& P) {
   __shared__ int scan[33];
+  __shared__ int s_entries[S ? kPagesSmallSlots : 1];
   pdl_wait();
   pdl_trigger();
-  const int ps = 1 << P.page_shift;
-  const int c = (int)cluster_ctarank();
-  auto need = [&](int r) -> long long {
+  const int ps = 1 << P.page_shift, mp = P.max_pages;
+  int bad = 0;
+  for (unsigned r = threadIdx.x; r < (unsigned)P.slots; r += kPagesThreads) {
     const int e = P.entries[r];
-    return e <= 0 ? 0 : ((long long)e + ps - 1) >> P.page_shift;
+    if (S) s_entries[r] = e;
+    if (e < 0 || (long long)e > ((long long)mp << P.page_shift)) bad = 1;
+  }
+  __syncthreads();
+  auto need = [&](int r) -> int {
+    const int e = S ? s_entries[r] : P.entries[r];
+    return e <= 0 ? 0 : (int)(((long long)e + ps - 1) >> P.page_shift);
   };
-  long long t0, t1, f0, f1;
-  my_run((long long)P.slots * P.max_pages, t0, t1);
-  my_run(P.num_pages, f0, f1);
-  int want = 0, bad = 0;
-  for (long long i = t0; i < t1; ++i) {
-    const int r = (int)(i / P.max_pages), lp = (int)(i - (long long)r * P.max_pages);
-    const long long n = need(r);
-    if (lp == 0 && (n > P.max_pages || P.entries[r] < 0)) bad = 1;
-    const int v = P.table[i];
+  unsigned t0, t1, f0, f1;
+  my_run<C>((unsigned)P.slots * mp, t0, t1);
+  my_run<C>((unsigned)P.num_pages, f0, f1);
+  int want = 0, nfree = 0;
+  batched(t1, t0, 1, [&](unsigned i) { return P.table[i]; }, [&](unsigned i, int v) {
+    const unsigned r = i / (unsigned)mp;
     if (v < -1 || v >= P.num_pages) bad = 1;
-    if (lp < n && v < 0) ++want;
-  }
-  int nfree = 0;
-  for (long long i = f0; i < f1; ++i) nfree += P.refs[i] == 0 ? 1 : 0;
-  int wtot, ftot, btot;
-  const int wpos = block_scan(want, scan, wtot);
-  const int fpos = block_scan(nfree, scan, ftot);
-  block_scan(bad, scan, btot);
-  if (threadIdx.x == 0) {
-    P.counts[c] = wtot;
-    P.counts[kPagesCluster + c] = ftot;
-    P.counts[2 * kPagesCluster + c] = btot;
-  }
-  cluster_sync();
+    if (v < 0 && (int)(i - r * mp) < need(r)) ++want;
+  });
+  batched(f1, f0, 1, [&](unsigned i) { return P.refs[i]; }, [&](unsigned, int v) { nfree += v == 0 ? 1 : 0; });
   int wall, fall, ball;
-  int w = cluster_prefix(P.counts, 0, wall) + wpos;
-  int f = cluster_prefix(P.counts, 1, fall) + fpos;
-  cluster_prefix(P.counts, 2, ball);
+  int w = all_scan<C>(want, scan, P.counts, 0, wall);
+  int f = all_scan<C>(nfree, scan, P.counts, 1, fall);
+  all_scan<C>(bad, scan, P.counts, 2, ball);
   if (ball > 0 || wall > fall) {  // the same in every thread
-    if (c == 0 && threadIdx.x == 0) record_status(P.status, ball > 0 ? CSA_DEV_BOUNDS : CSA_DEV_NO_PAGES);
-    cluster_sync();
+    if (rank<C>() == 0 && threadIdx.x == 0) record_status(P.status, ball > 0 ? CSA_DEV_BOUNDS : CSA_DEV_NO_PAGES);
     return;
   }
-  for (long long i = f0; i < f1 && f < wall; ++i)
+  if (wall == 0) return;
+  for (unsigned i = f0; i < f1 && f < wall; ++i)
     if (P.refs[i] == 0) {
       P.list_a[f++] = (int)i;
       P.refs[i] = 1;
     }
-  cluster_sync();
+  all_sync<C>();
   if (want > 0)
-    for (long long i = t0; i < t1; ++i) {
-      const int r = (int)(i / P.max_pages), lp = (int)(i - (long long)r * P.max_pages);
-      if (lp < need(r) && P.table[i] < 0) P.table[i] = ld_cg(P.list_a + w++);
+    for (unsigned i = t0; i < t1; ++i) {
+      const unsigned r = i / (unsigned)mp;
+      if ((int)(i - r * mp) < need(r) && P.table[i] < 0) P.table[i] = ld_cg(P.list_a + w++);
     }
 }
 
@@ -332,164 +362,149 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
 // reference, except that of several heirs of a partly filled last page one keeps it (the parent's own slot, else
 // the lowest heir) and the others get fresh pages, which pages_copy_kernel fills. Nothing is committed before the
 // free pages are known to suffice: reference counts are worked out in `list_b`, changed rows in `rows`.
-__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads) pages_fork_kernel(PagesParams P) {
+template <int C, bool S>
+__device__ __forceinline__ void pages_fork(const PagesParams& P) {
   __shared__ int scan[33];
+  __shared__ int s_parent[S ? kPagesSmallSlots : 1], s_need[S ? kPagesSmallSlots : 1], s_copy[S ? kPagesSmallSlots : 1];
+  __shared__ int s_heir[S ? kPagesSmallSlots : 1];
   pdl_wait();
   pdl_trigger();
-  const int ps = 1 << P.page_shift;
-  const int c = (int)cluster_ctarank();
-  const int tid = c * kPagesThreads + threadIdx.x;
-  constexpr int kAll = kPagesCluster * kPagesThreads;
-  const int cap = P.max_pages << P.page_shift;
+  const unsigned tid = rank<C>() * kPagesThreads + threadIdx.x;
+  constexpr unsigned kAll = C * kPagesThreads;
+  const int ps = 1 << P.page_shift, cap = P.max_pages << P.page_shift;
+  const unsigned cells = (unsigned)P.slots * P.max_pages, mp = P.max_pages;
+  // Slots are walked by every CTA where their arrays are its own, by all together otherwise.
+  const unsigned s_first = S ? threadIdx.x : tid, s_step = S ? kPagesThreads : kAll;
+  int* heir = S ? s_heir : P.heir;
+  int* need = S ? s_need : P.need;    // pages that the slot takes over
+  int* copy = S ? s_copy : P.copy;    // the place of which it takes a copy, -1: none
+  auto at = [](int* p, unsigned i) { return S ? p[i] : ld_cg(p + i); };
+  auto parent_of = [&](unsigned r) { return S ? s_parent[r] : P.parent[r]; };
   // Phase 0: check, copy the counts, clear the heirs.
   int bad = 0;
-  for (int r = tid; r < P.slots; r += kAll) {
+  for (unsigned r = s_first; r < (unsigned)P.slots; r += s_step) {
     const int p = P.parent[r], e = P.entries[r];
     if (p < -1 || p >= P.slots || e < 0 || e > cap) bad = 1;
-    P.heir[r] = 0x7FFFFFFF;
+    if (S) s_parent[r] = p;
+    heir[r] = 0x7FFFFFFF;
   }
-  const long long cells = (long long)P.slots * P.max_pages;
-  for (long long i = tid; i < cells; i += kAll) {
-    const int v = P.table[i];
+  batched(cells, tid, kAll, [&](unsigned i) { return P.table[i]; }, [&](unsigned, int v) {
     if (v < -1 || v >= P.num_pages) bad = 1;
-  }
-  for (int i = tid; i < P.num_pages; i += kAll) P.list_b[i] = P.refs[i];
-  int btot;
-  block_scan(bad, scan, btot);
-  if (threadIdx.x == 0) P.counts[c] = btot;
+  });
+  batched((unsigned)P.num_pages, tid, kAll, [&](unsigned i) { return P.refs[i]; }, [&](unsigned i, int v) { P.list_b[i] = v; });
   if (tid == 0) *P.n_moves = 0;
-  cluster_sync();
   int ball;
-  cluster_prefix(P.counts, 0, ball);
+  all_scan<C>(bad, scan, P.counts, 0, ball);
   if (ball > 0) {
     if (tid == 0) record_status(P.status, CSA_DEV_BOUNDS);
-    cluster_sync();
     return;
   }
-  // Phase 1: the lowest heir of each slot that does not keep itself.
-  for (int r = tid; r < P.slots; r += kAll) {
-    const int s = P.parent[r];
-    if (s >= 0) atomicMin(P.heir + s, s == r ? -1 : r);
+  // Phase 1: the lowest heir of each slot that does not keep itself; what each slot takes.
+  for (unsigned r = s_first; r < (unsigned)P.slots; r += s_step) {
+    const int s = parent_of(r);
+    if (s >= 0) atomicMin(heir + s, s == (int)r ? -1 : (int)r);
   }
-  cluster_sync();
-  // Slot r takes a copy of its parent's last page?
-  auto copies = [&](int r, int& s, int& lp) -> bool {
-    s = P.parent[r];
-    if (s < 0 || s == r || (P.entries[s] & (ps - 1)) == 0 || ld_cg(P.heir + s) == r) return false;
-    lp = P.entries[s] >> P.page_shift;
-    return P.table[(long long)s * P.max_pages + lp] >= 0;
-  };
-  // Phase 2: changed rows and counts.
-  for (long long i = tid; i < cells; i += kAll) {
-    const int r = (int)(i / P.max_pages), lp = (int)(i - (long long)r * P.max_pages);
-    const int s = P.parent[r];
-    if (s == r) continue;
-    const int was = P.table[i];
-    if (was >= 0) atomicAdd(P.list_b + was, -1);
-    int now = -1;
-    if (s >= 0 && lp < (int)(((long long)P.entries[s] + ps - 1) >> P.page_shift)) {
-      now = P.table[(long long)s * P.max_pages + lp];
-      int s2, lp2;
-      if (now >= 0 && !(copies(r, s2, lp2) && lp2 == lp)) atomicAdd(P.list_b + now, 1);
+  S ? __syncthreads() : all_sync<C>();
+  for (unsigned r = s_first; r < (unsigned)P.slots; r += s_step) {
+    const int s = parent_of(r);
+    int n = 0, c = -1;
+    if (s >= 0 && s != (int)r) {
+      const int e = P.entries[s];
+      n = (int)(((long long)e + ps - 1) >> P.page_shift);
+      if ((e & (ps - 1)) != 0 && at(heir, s) != (int)r && P.table[s * mp + n - 1] >= 0) c = n - 1;
     }
-    P.rows[i] = now;
+    need[r] = n;
+    copy[r] = c;
   }
+  S ? __syncthreads() : all_sync<C>();
+  // Phase 2: changed rows and counts.
+  batched(cells, tid, kAll,
+          [&](unsigned i) {
+            const unsigned r = i / mp, lp = i - r * mp;
+            const int s = parent_of(r);
+            if (s == (int)r) return make_int2(-1, -1);
+            return make_int2(P.table[i], (int)lp < at(need, r) ? P.table[s * mp + lp] : -1);
+          },
+          [&](unsigned i, int2 v) {  // (what the place held, what it takes over)
+            const unsigned r = i / mp, lp = i - r * mp;
+            if (parent_of(r) == (int)r) return;
+            if (v.x >= 0) atomicAdd(P.list_b + v.x, -1);
+            if (v.y >= 0 && at(copy, r) != (int)lp) atomicAdd(P.list_b + v.y, 1);
+            P.rows[i] = v.y;
+          });
   int want = 0;
-  long long r0, r1, f0, f1;
-  my_run(P.slots, r0, r1);
-  my_run(P.num_pages, f0, f1);
-  for (long long r = r0; r < r1; ++r) {
-    int s, lp;
-    want += copies((int)r, s, lp) ? 1 : 0;
-  }
-  int wtot;
-  const int wpos = block_scan(want, scan, wtot);
-  if (threadIdx.x == 0) P.counts[kPagesCluster + c] = wtot;
-  cluster_sync();
-  // Phase 3: free pages.
-  int nfree = 0, ftot;
-  for (long long i = f0; i < f1; ++i) nfree += ld_cg(P.list_b + i) == 0 ? 1 : 0;
-  const int fpos = block_scan(nfree, scan, ftot);
-  if (threadIdx.x == 0) P.counts[2 * kPagesCluster + c] = ftot;
-  cluster_sync();
+  unsigned r0, r1, f0, f1;
+  my_run<C>((unsigned)P.slots, r0, r1);
+  my_run<C>((unsigned)P.num_pages, f0, f1);
+  for (unsigned r = r0; r < r1; ++r) want += at(copy, r) >= 0 ? 1 : 0;
   int wall, fall;
-  int w = cluster_prefix(P.counts, 1, wall) + wpos;
-  int f = cluster_prefix(P.counts, 2, fall) + fpos;
+  int w = all_scan<C>(want, scan, P.counts, 1, wall);
+  // Phase 3: free pages.
+  int nfree = 0;
+  batched(f1, f0, 1, [&](unsigned i) { return ld_cg(P.list_b + i); }, [&](unsigned, int v) { nfree += v == 0 ? 1 : 0; });
+  int f = all_scan<C>(nfree, scan, P.counts, 2, fall);
   if (wall > fall) {
     if (tid == 0) record_status(P.status, CSA_DEV_NO_PAGES);
-    cluster_sync();
     return;
   }
-  for (long long i = f0; i < f1; ++i) {
-    const int v = ld_cg(P.list_b + i);
-    int now = v;
+  batched(f1, f0, 1, [&](unsigned i) { return ld_cg(P.list_b + i); }, [&](unsigned i, int v) {
     if (v == 0 && f < wall) {
       P.list_a[f++] = (int)i;
-      now = 1;
+      v = 1;
     }
-    P.refs[i] = now;
-  }
-  cluster_sync();
+    P.refs[i] = v;
+  });
+  all_sync<C>();
   // Phase 4: the moves and the changed places (the parents' rows are read before any row changes).
-  for (long long r = r0; r < r1; ++r) {
-    int s, lp;
-    if (!copies((int)r, s, lp)) continue;
+  for (unsigned r = r0; r < r1; ++r) {
+    const int lp = at(copy, r);
+    if (lp < 0) continue;
     const int dst = ld_cg(P.list_a + w);
-    P.move_src[w] = P.table[(long long)s * P.max_pages + lp];
+    P.move_src[w] = P.table[(unsigned)parent_of(r) * mp + lp];
     P.move_dst[w] = dst;
     ++w;
-    P.rows[r * P.max_pages + lp] = dst;
+    P.rows[r * mp + lp] = dst;
   }
   if (tid == 0) *P.n_moves = wall;
-  cluster_sync();
-  for (long long i = tid; i < cells; i += kAll) {
-    const int r = (int)(i / P.max_pages);
-    if (P.parent[r] != r) P.table[i] = ld_cg(P.rows + i);
-  }
+  all_sync<C>();
+  batched(cells, tid, kAll, [&](unsigned i) { return ld_cg(P.rows + i); }, [&](unsigned i, int v) {
+    if (parent_of(i / mp) != (int)(i / mp)) P.table[i] = v;
+  });
 }
 
 // Live pages (refs > 0) move to the front: with L of them, the k-th live page at or behind L goes to the k-th
 // free page before L. map[p]: where page p is now (-1: it was free).
-__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads) pages_compact_kernel(PagesParams P) {
+template <int C, bool>
+__device__ __forceinline__ void pages_compact(const PagesParams& P) {
   __shared__ int scan[33];
   pdl_wait();
   pdl_trigger();
-  const int c = (int)cluster_ctarank();
-  const int tid = c * kPagesThreads + threadIdx.x;
-  constexpr int kAll = kPagesCluster * kPagesThreads;
-  long long f0, f1;
-  my_run(P.num_pages, f0, f1);
-  int nlive = 0, ltot;
-  for (long long i = f0; i < f1; ++i) nlive += P.refs[i] != 0 ? 1 : 0;
-  const int pos = block_scan(nlive, scan, ltot);
-  if (threadIdx.x == 0) P.counts[c] = ltot;
-  cluster_sync();
-  int L;
-  const int before = cluster_prefix(P.counts, 0, L) + pos;  // live pages before f0
+  const unsigned tid = rank<C>() * kPagesThreads + threadIdx.x;
+  constexpr unsigned kAll = C * kPagesThreads;
+  unsigned f0, f1;
+  my_run<C>((unsigned)P.num_pages, f0, f1);
+  int nlive = 0, L;
+  batched(f1, f0, 1, [&](unsigned i) { return P.refs[i]; }, [&](unsigned, int v) { nlive += v != 0 ? 1 : 0; });
+  const int before = all_scan<C>(nlive, scan, P.counts, 0, L);  // live pages before f0
   // Holes (free pages before L), numbered from the front. As many live pages lie at or behind L, and L - 1 - k of
   // them follow page i with k live pages before it, so its number from the front is M - 1 - (L - 1 - k).
-  int holes = 0;
-  for (long long i = f0, k = before; i < f1; ++i) {
+  int holes = 0, M;
+  for (int i = (int)f0, k = before; i < (int)f1; ++i) {
     const bool live = P.refs[i] != 0;
     if (!live && i < L) {
-      P.list_a[i - k] = (int)i;
+      P.list_a[i - k] = i;
       ++holes;
     }
     k += live ? 1 : 0;
   }
-  int htot;
-  block_scan(holes, scan, htot);
-  if (threadIdx.x == 0) P.counts[kPagesCluster + c] = htot;
-  cluster_sync();
-  int M;
-  cluster_prefix(P.counts, 1, M);
-  for (long long i = f0, k = before; i < f1; ++i) {
+  all_scan<C>(holes, scan, P.counts, 1, M);
+  for (int i = (int)f0, k = before; i < (int)f1; ++i) {
     const bool live = P.refs[i] != 0;
-    int to = live ? (int)i : -1;
+    int to = live ? i : -1;
     if (live && i >= L) {
-      const int m = M - 1 - (int)(L - 1 - k);
+      const int m = M - 1 - (L - 1 - k);
       to = ld_cg(P.list_a + m);
-      P.move_src[m] = (int)i;
+      P.move_src[m] = i;
       P.move_dst[m] = to;
     }
     P.map[i] = to;
@@ -499,21 +514,35 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
     *P.n_moves = M;
     *P.live = L;
   }
-  cluster_sync();
+  all_sync<C>();
   for (int m = tid; m < M; m += kAll) {
     const int src = ld_cg(P.move_src + m), dst = ld_cg(P.move_dst + m);
     P.refs[dst] = P.refs[src];
     P.refs[src] = 0;
   }
-  const long long cells = (long long)P.slots * P.max_pages;
-  for (long long i = tid; i < cells; i += kAll) {
-    const int v = P.table[i];
-    if (v == -1) continue;
-    const int to = v >= 0 && v < P.num_pages ? ld_cg(P.map + v) : -1;
-    if (to < 0) record_status(P.status, CSA_DEV_BOUNDS);  // a place that maps no live page: left as it is
-    else if (to != v) P.table[i] = to;
-  }
+  batched((unsigned)P.slots * P.max_pages, tid, kAll,
+          [&](unsigned i) {
+            const int v = P.table[i];
+            return make_int2(v, v >= 0 && v < P.num_pages ? ld_cg(P.map + v) : -1);
+          },
+          [&](unsigned i, int2 v) {  // (page, where it is now)
+            if (v.x == -1) return;
+            if (v.y < 0) record_status(P.status, CSA_DEV_BOUNDS);  // a place that maps no live page: left as it is
+            else if (v.y != v.x) P.table[i] = v.y;
+          });
 }
+
+#define CSA_PAGES_KERNELS(name)                                                                                        \
+  __global__ void __launch_bounds__(kPagesThreads) name##_kernel(PagesParams P) { name<1, true>(P); }                   \
+  __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)                                 \
+      name##_cluster_kernel(PagesParams P) {                                                                            \
+    if (P.slots <= kPagesSmallSlots) name<kPagesCluster, true>(P);                                                      \
+    else name<kPagesCluster, false>(P);                                                                                 \
+  }
+CSA_PAGES_KERNELS(pages_reserve)
+CSA_PAGES_KERNELS(pages_fork)
+CSA_PAGES_KERNELS(pages_compact)
+#undef CSA_PAGES_KERNELS
 
 // The moves of a fork or a compaction, in every pool: work unit = (move, chunk of a pool's page), 16 bytes a thread
 // and load, four loads in flight. Sources and destinations of one call never overlap. Bound by DRAM: a page's bytes

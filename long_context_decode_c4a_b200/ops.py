@@ -25,7 +25,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # The raw handle of torch.cuda.current_stream(), which builds a Stream object each time (3 us of a call of 10).
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
@@ -33,9 +34,9 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the layer runs only in libcsa.so's kernels)")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -494,12 +495,12 @@ def window_projection(x: torch.Tensor, wkv: torch.Tensor, pos: torch.Tensor, rop
 # ------------------------------------------------------------------------------------------------ caches in pages
 
 
-def _same_device(device: torch.device, *tensors) -> None:
+def _same_device(device: int, *tensors) -> None:
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {t.device} and {device} in one call")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}: make it the current device (torch.cuda.device) for the call")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on {t.device} and cuda:{device} in one call")
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{device}: make it the current device (torch.cuda.device) for the call")
 
 
 class PageTable:
@@ -521,10 +522,11 @@ class PageTable:
         self.slots, self.max_pages = table.shape
         self.num_pages = refs.shape[0]
         self.max_entries = self.max_pages * page_size
-        self.device = table.device
+        self.device, self._index = table.device, table.get_device()
         self.ws = workspace(_lib.CSA_WS_PAGES, self.slots, self.max_pages, self.num_pages, 0, table.device)
+        self._ws = self.ws.data_ptr(), self.ws.numel()
         self._arg = PageTableArg(self.slots, self.max_pages, self.num_pages, page_size, table.data_ptr(), refs.data_ptr())
-        self._ref = ctypes.byref(self._arg)
+        self._ref, self._addr = ctypes.byref(self._arg), ctypes.addressof(self._arg)
 
     @classmethod
     def empty(cls, slots: int, max_pages: int, num_pages: int, page_size: int = 64, device="cuda") -> "PageTable":
@@ -556,7 +558,7 @@ class PagedCache:
             raise ValueError("the cache must be on its page table's device")
         self.book, self.pages, self.scales, self.block, self.d = book, pages, scales, block, pages.shape[2]
         self._arg = PagedCacheArg(self.d, block, pages.data_ptr(), _ptr(scales))
-        self._ref = ctypes.byref(self._arg)
+        self._ref, self._addr = ctypes.byref(self._arg), ctypes.addressof(self._arg)
 
     @classmethod
     def e4m3(cls, book: PageTable, block: int = 16) -> "PagedCache":
@@ -590,9 +592,9 @@ def cache_append(cache: PagedCache, start_pos: torch.Tensor, S: int, rows: torch
         raise ValueError(f"start_pos must be [B] and rows [B, max_rows, {cache.d}]")
     if rows.dtype != torch.bfloat16:
         raise TypeError(f"rows must be {torch.bfloat16}, got {rows.dtype}")
-    _same_device(book.device, start_pos, rows)
+    _same_device(book._index, start_pos, rows)
     check(_lib.load().csa_cache_append(book._ref, cache._ref, B, S, ratio, start_pos.data_ptr(), rows.data_ptr(),
-                                       _bstride(rows, "rows"), rows.shape[1], book.ws.data_ptr(), book.ws.numel(),
+                                       _bstride(rows, "rows"), rows.shape[1], *book._ws,
                                        _stream()), "csa_cache_append")
 
 
@@ -606,17 +608,16 @@ def cache_read(cache: PagedCache, idx: torch.Tensor, out: Optional[torch.Tensor]
     if out is None:
         out = torch.zeros(B, n, cache.d, dtype=torch.bfloat16, device=idx.device)
     _need(out, "out", torch.bfloat16, (B, n, cache.d))
-    _same_device(book.device, idx, out)
-    check(_lib.load().csa_cache_read(book._ref, cache._ref, B, n, idx.data_ptr(), out.data_ptr(), book.ws.data_ptr(),
-                                     book.ws.numel(), _stream()), "csa_cache_read")
+    _same_device(book._index, idx, out)
+    check(_lib.load().csa_cache_read(book._ref, cache._ref, B, n, idx.data_ptr(), out.data_ptr(), *book._ws, _stream()), "csa_cache_read")
     return out
 
 
 def pages_reserve(book: PageTable, entries: torch.Tensor) -> None:
     """Map pages for entries[r] (int32 [slots]) entries of every slot: the lowest free pages, in slot order."""
     _need(entries, "entries", torch.int32, (book.slots,))
-    _same_device(book.device, entries)
-    check(_lib.load().csa_pages_reserve(book._ref, entries.data_ptr(), book.ws.data_ptr(), book.ws.numel(), _stream()),
+    _same_device(book._index, entries)
+    check(_lib.load().csa_pages_reserve(book._ref, entries.data_ptr(), *book._ws, _stream()),
           "csa_pages_reserve")
 
 
@@ -626,9 +627,9 @@ def pages_fork(book: PageTable, caches, parent: torch.Tensor, entries: torch.Ten
     (all behind `book`). parent, entries: int32 [slots]."""
     _need(parent, "parent", torch.int32, (book.slots,))
     _need(entries, "entries", torch.int32, (book.slots,))
-    _same_device(book.device, parent, entries)
+    _same_device(book._index, parent, entries)
     check(_lib.load().csa_pages_fork(book._ref, _cache_list(book, caches), len(caches), parent.data_ptr(),
-                                     entries.data_ptr(), book.ws.data_ptr(), book.ws.numel(), _stream()),
+                                     entries.data_ptr(), *book._ws, _stream()),
           "csa_pages_fork")
 
 
@@ -641,9 +642,9 @@ def pages_compact(book: PageTable, caches, map: Optional[torch.Tensor] = None, l
         live = torch.empty(1, dtype=torch.int32, device=book.device)
     _need(map, "map", torch.int32, (book.num_pages,))
     _need(live, "live", torch.int32, (1,))
-    _same_device(book.device, map, live)
+    _same_device(book._index, map, live)
     check(_lib.load().csa_pages_compact(book._ref, _cache_list(book, caches), len(caches), map.data_ptr(),
-                                        live.data_ptr(), book.ws.data_ptr(), book.ws.numel(), _stream()),
+                                        live.data_ptr(), *book._ws, _stream()),
           "csa_pages_compact")
     return map, live
 
@@ -668,7 +669,7 @@ def indexer_scores_paged(q_pos: torch.Tensor, q_idx: torch.Tensor, w: torch.Tens
     _need(scores, "scores", torch.float32, (B, S, book.max_entries))
     if ws is None:
         ws = workspace(_lib.CSA_WS_SPARSE_ATTN, B, S, 1, 1, q_idx.device)
-    _same_device(book.device, q_pos, q_idx, w, scores, ws)
+    _same_device(book._index, q_pos, q_idx, w, scores, ws)
     check(_lib.load().csa_indexer_scores_paged(book._ref, cache._ref, B, S, H_I, ratio, q_pos.data_ptr(),
                                                q_idx.data_ptr(), w.data_ptr(), scores.data_ptr(), ws.data_ptr(),
                                                ws.numel(), _stream()), "csa_indexer_scores_paged")
@@ -688,7 +689,7 @@ def indexer_topk_paged(q_pos: torch.Tensor, q_idx: torch.Tensor, w: torch.Tensor
         _need(scores, "scores", torch.float32, (B, S, book.max_entries))
     if ws is None:
         ws = workspace(_lib.CSA_WS_INDEXER_TOPK, B, S, book.max_entries, topk, q_idx.device)
-    _same_device(book.device, q_pos, q_idx, w, topk_idx, scores, ws)
+    _same_device(book._index, q_pos, q_idx, w, topk_idx, scores, ws)
     check(_lib.load().csa_indexer_topk_paged(book._ref, cache._ref, B, S, H_I, ratio, topk, q_pos.data_ptr(),
                                              q_idx.data_ptr(), w.data_ptr(), topk_idx.data_ptr(), _ptr(scores),
                                              ws.data_ptr(), ws.numel(), _stream()), "csa_indexer_topk_paged")
@@ -728,12 +729,11 @@ def sparse_attn8(q_pos: torch.Tensor, q: torch.Tensor, ring: torch.Tensor, cache
     if ws is None:
         ws = workspace(_lib.CSA_WS_SPARSE_ATTN, B, S, 1, 1, q.device)
     book = cache.book
-    _same_device(book.device, q_pos, q, ring, topk_idx, sink, out, ws)
-    check(_lib.load().csa_sparse_attn8(book._ref, cache._ref, B, S, H, rope_dim, rope_base, scale, ratio,
-                                       q_pos.data_ptr(), q.data_ptr(), ring.data_ptr(), _bstride(ring, "ring"),
-                                       ring.shape[1], window, topk_idx.data_ptr(), topk_idx.shape[2], sink.data_ptr(),
-                                       out.data_ptr(), int(out.dtype == torch.float32), ws.data_ptr(), ws.numel(),
-                                       _stream()), "csa_sparse_attn8")
+    _same_device(book._index, q_pos, q, ring, topk_idx, sink, out, ws)
+    a = _lib.pack_attn8(book._addr, cache._addr, q_pos.data_ptr(), q.data_ptr(), ring.data_ptr(), topk_idx.data_ptr(),
+                        sink.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(), _bstride(ring, "ring"), B, S, H, rope_dim,
+                        rope_base, scale, ratio, ring.shape[1], window, topk_idx.shape[2], out.dtype is torch.float32)
+    check(_lib.load().csa_sparse_attn8(a, _stream()), "csa_sparse_attn8")
     return out
 
 
@@ -746,11 +746,11 @@ def hca_attn8(q_pos: torch.Tensor, q: torch.Tensor, ring: torch.Tensor, cache: P
     if ws is None:
         ws = workspace(_lib.CSA_WS_HCA_ATTN, B, S, 1, 1, q.device)
     book = cache.book
-    _same_device(book.device, q_pos, q, ring, sink, out, ws)
-    check(_lib.load().hca_attn8(book._ref, cache._ref, B, S, H, rope_dim, rope_base, scale, ratio, q_pos.data_ptr(),
-                                q.data_ptr(), ring.data_ptr(), _bstride(ring, "ring"), ring.shape[1], window,
-                                sink.data_ptr(), out.data_ptr(), int(out.dtype == torch.float32), ws.data_ptr(),
-                                ws.numel(), _stream()), "hca_attn8")
+    _same_device(book._index, q_pos, q, ring, sink, out, ws)
+    a = _lib.pack_attn8(book._addr, cache._addr, q_pos.data_ptr(), q.data_ptr(), ring.data_ptr(), 0, sink.data_ptr(),
+                        out.data_ptr(), ws.data_ptr(), ws.numel(), _bstride(ring, "ring"), B, S, H, rope_dim, rope_base, scale,
+                        ratio, ring.shape[1], window, 0, out.dtype is torch.float32)
+    check(_lib.load().hca_attn8(a, _stream()), "hca_attn8")
     return out
 
 

@@ -43,7 +43,7 @@ def same_book(book, table, refs):
 # ------------------------------------------------------------------------------------------------ page table
 
 
-@pytest.mark.parametrize("slots,max_pages,page", [(1, 1, 16), (3, 5, 16), (64, 130, 64), (700, 13, 1024), (1, 20000, 64)])
+@pytest.mark.parametrize("slots,max_pages,page", [(1, 1, 16), (3, 5, 16), (64, 130, 64), (700, 13, 1024), (1, 20000, 64), (2100, 5, 16)])
 def test_reserve(ops, slots, max_pages, page):
     g = torch.Generator().manual_seed(slots)
     used = torch.randint(0, max_pages + 1, (slots,), generator=g).tolist()
@@ -74,7 +74,7 @@ def test_reserve_out_of_range(ops, entries):
     same_book(book, [[-1] * 4] * 2, [0] * 8)
 
 
-@pytest.mark.parametrize("seed,slots,max_pages,page", [(0, 1, 3, 16), (1, 4, 3, 16), (2, 9, 7, 32), (3, 64, 40, 64), (4, 300, 9, 16)])
+@pytest.mark.parametrize("seed,slots,max_pages,page", [(0, 1, 3, 16), (1, 4, 3, 16), (2, 9, 7, 32), (3, 64, 40, 64), (4, 300, 9, 16), (5, 2500, 3, 16)])
 def test_fork_keep_free(ops, seed, slots, max_pages, page):
     """Random parent maps (kept, copied, swapped and freed slots), several in a row, with the rows that follow the pages."""
     g = torch.Generator().manual_seed(seed)

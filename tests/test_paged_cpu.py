@@ -18,12 +18,19 @@ def lib():
     return _lib.load()
 
 
-@pytest.mark.parametrize("cls,cname", [(_lib.PageTableArg, "csa_page_table"), (_lib.PagedCacheArg, "csa_paged_cache")])
+@pytest.mark.parametrize("cls,cname", [(_lib.PageTableArg, "csa_page_table"), (_lib.PagedCacheArg, "csa_paged_cache"),
+                                       (_lib.Attn8Args, "csa_attn8_args")])
 def test_struct_layout_matches_header(cls, cname):
     fields = [f for f, _ in cls._fields_]
     size, offs = _c_offsets(cname, fields)
     assert ctypes.sizeof(cls) == size
     assert [getattr(cls, f).offset for f in fields] == offs
+
+
+def test_packed_attention_arguments():
+    values = [4096 + i for i in range(9)] + [1 << 33, -(1 << 40), 1, 2, 3, 4, 1e4, 0.5, 5, 6, 7, 8, 1]
+    a = _lib.Attn8Args.from_buffer_copy(_lib.pack_attn8(*values))
+    assert [getattr(a, f) for f, _ in _lib.Attn8Args._fields_] == values
 
 
 def test_status_string(lib):
@@ -66,10 +73,12 @@ def calls(lib, pt, c8, c16, ws=P, ws_bytes=1 << 20):
         pt, c16, B, S, H, ratio, P, q, P, scores, ws, ws_bytes, None)
     yield "topk", lambda B=2, S=1, H=64, ratio=4, k=16, idx=P: lib.csa_indexer_topk_paged(
         pt, c16, B, S, H, ratio, k, P, P, P, idx, None, ws, ws_bytes, None)
-    yield "list", lambda B=2, S=1, H=128, rd=64, base=1e4, scale=0.1, ratio=4, q=P, ring=P, stride=512 * 128, cap=128, win=128, idx=P, k=8: \
-        lib.csa_sparse_attn8(pt, c8, B, S, H, rd, base, scale, ratio, P, q, ring, stride, cap, win, idx, k, P, P, 0, ws, ws_bytes, None)
-    yield "range", lambda B=2, S=1, H=128: lib.hca_attn8(
-        pt, c8, B, S, H, 64, 1e4, 0.1, 4, P, P, P, 512 * 128, 128, 128, P, P, 0, ws, ws_bytes, None)
+    def attn(fn, B=2, S=1, H=128, rd=64, base=1e4, scale=0.1, ratio=4, q=P, ring=P, stride=512 * 128, cap=128, win=128, idx=P, k=8):
+        addr = lambda x: ctypes.cast(x, ctypes.c_void_p).value if x is not None else None  # noqa: E731
+        a = _lib.Attn8Args(addr(pt), addr(c8), P, q, ring, idx, P, P, ws, ws_bytes, stride, B, S, H, rd, base, scale, ratio, cap, win, k, 0)
+        return fn(ctypes.addressof(a), None)
+    yield "list", lambda **kw: attn(lib.csa_sparse_attn8, **kw)
+    yield "range", lambda **kw: attn(lib.hca_attn8, **kw)
 
 
 @pytest.mark.parametrize("bad,code", [

@@ -24,7 +24,7 @@
 // y_j = l_j + log2 s_j; the denominator takes P back to p_j with 1 / s_j. The sink enters at the end
 // only: it must not push P below e4m3's range.
 //
-// Layout: two CTAs per query; CTA `half` accumulates O[:, 256 half .. 256 half + 256) (128 heads x 256
+// Layout: a cluster of two CTAs per query; CTA `half` accumulates O[:, 256 half .. 256 half + 256) (128 heads x 256
 // columns of fp32 are half of TMEM) and computes the scores over all 512 dims itself. Both CTAs so gather
 // whole rows: 512 bytes, as many as the half row of a bf16 cache, and no partial score crosses the pair.
 //   TMEM (512 columns): [0,128) q1 (four codes a column); [128,192) the scores of a 64-row tile; [192,224)
@@ -32,6 +32,8 @@
 //     as they are there, so the score MMAs of the next tile run during the softmax of this one.
 //   SMEM: four 32 KB stages of 64 rows (four 128-byte blocks in the 128B-swizzled layout, which serves the
 //     scores as a K-major and PV as an MN-major operand); q2 (64 KB).
+//   Each CTA splits half of q's heads and half of every window tile's rows and writes the pieces into both CTAs'
+//     shared memory (the splits are bound by integer and conversion rates: whole ones cost 8 us a query more).
 //   Warps: 0..3 split window rows and gather entries (16-byte cp.async, a warp covering one row an
 //     instruction); 4 issues the score MMAs, 5 the PV MMAs (and owns TMEM); 6..9 and 10..13 are the softmax groups
 //     of even and odd tiles, one head (TMEM lane) a thread; both first split q, and share the epilogue.
@@ -71,12 +73,15 @@ constexpr float kHead = 4.25f, kOver = 0.75f;
 static_assert(kAttn8Threads == 32 * (kSoftWarp + 8), "warp roles");
 
 struct Smem8 {
-  uint64_t kv_full[kStages8], kv_free[kStages8];
+  uint64_t kv_full[kStages8];  // this CTA's rows of the stage are there
+  uint64_t wr_full[kStages8];  // ... and the other CTA's, for a window tile
+  uint64_t kv_free[kStages8];  // PV of the stage's tile completed in both CTAs
   uint64_t s_full[2];      // the scores of tile j are written (barrier j % 2: a group looks at its own tiles only)
   uint64_t s_free;         // ... and have left for registers (phase j)
   uint64_t p_full[2];      // P of tile j stored (P buffer j % 2)
   uint64_t pv_done[4];     // PV(j) completed (barrier j % 4): its P buffer is free, O holds PV(0..j)
-  uint64_t q_done;         // q1 is in TMEM, q2 in shared memory, the staging area (stages 2, 3) is free
+  uint64_t q_ready;        // both CTAs' pieces of q are in shared memory
+  uint64_t q_done;         // q1 is in TMEM in both CTAs: the staging area (stages 2, 3) is free
   uint64_t list_ready;
   uint64_t hand[2][4];     // softmax group g published the running maximum after its tile (quadrant q)
   uint64_t drain[2];
@@ -163,12 +168,20 @@ __device__ __forceinline__ float split_row(const uint4& a, const uint4& b, RowPi
   return e < 255 ? __uint_as_float((uint32_t)(127 + k) << 23) : CUDART_NAN_F;
 }
 
-// Store lane l's 8 + 8 codes of row `row` into a [4 blocks][rows][128 B] swizzled region of block size `blk`.
-__device__ __forceinline__ void store_codes(uint8_t* base, uint32_t blk, int row, int lane, const uint2 (&v)[2]) {
+// What a CTA gets from the other: of a window tile (16 rows, two pieces and two scales each), and of q (64 heads, two
+// pieces and a factor each).
+constexpr uint32_t kPeerTile = 16 * (2 * 512 + 2 * 4), kPeerQ = 64 * (2 * 512 + 4);
+
+// Store lane l's 8 + 8 codes of row `row` into a [4 blocks][rows][128 B] swizzled region of block size `blk`: of this
+// CTA (at `base`) and of the other (at cluster address `peer`, the bytes counted on its barrier `bar`).
+__device__ __forceinline__ void store_codes(uint8_t* base, uint32_t peer, uint32_t bar, uint32_t blk, int row, int lane, const uint2 (&v)[2]) {
   const uint32_t off = sw128_offset((uint32_t)row, (uint32_t)((lane & 15) >> 1)) + (uint32_t)(lane & 1) * 8u;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    *reinterpret_cast<uint2*>(base + (uint32_t)(2 * i + (lane >> 4)) * blk + off) = v[i];
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t at = (uint32_t)(2 * i + (lane >> 4)) * blk + off;
+    *reinterpret_cast<uint2*>(base + at) = v[i];
+    st_async_v2(peer + at, v[i].x, v[i].y, bar);
+  }
 }
 
 // Two 512-dim bf16 rows of a warp, as split_row takes them.
@@ -235,7 +248,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 }  // namespace
 
-__global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stages = base;
@@ -244,7 +257,8 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
   Smem8& sm = *reinterpret_cast<Smem8*>(q2 + kQ2Bytes);
 
   const int warp = warp_id(), lane = lane_id();
-  const int half = blockIdx.x & 1;
+  const int half = (int)cluster_ctarank();
+  const uint32_t peer = (uint32_t)half ^ 1u;
   const int nq = P.B * P.S;
   const int item = nq * P.splits - 1 - (int)(blockIdx.x >> 1);  // later queries (more candidates) first
   const int qi = item / P.splits, sp = item % P.splits, b = qi / P.S;
@@ -254,7 +268,8 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages8; ++i) {
       mbar_init(&sm.kv_full[i], kProd);
-      mbar_init(&sm.kv_free[i], 1);
+      mbar_init(&sm.wr_full[i], 1);
+      mbar_init(&sm.kv_free[i], 2);
     }
     mbar_init(&sm.s_free, kGroup);
     for (int i = 0; i < 2; ++i) {
@@ -263,7 +278,8 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
       for (int q = 0; q < 4; ++q) mbar_init(&sm.hand[i][q], 32);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&sm.pv_done[i], 1);
-    mbar_init(&sm.q_done, 2 * kGroup);
+    mbar_init(&sm.q_ready, 2 * kGroup + 1);
+    mbar_init(&sm.q_done, 4 * kGroup);
     mbar_init(&sm.list_ready, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.drain[i], 1);
     sm.abort_flag = 0;
@@ -275,8 +291,9 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // the barriers of both CTAs are initialised
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   pdl_wait();
@@ -295,46 +312,47 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
     const uint16_t* ring = P.ring + (long long)b * P.ring_bstride;
     const int32_t* sel = P.topk_idx == nullptr ? nullptr : P.topk_idx + (long long)qi * P.topk;
     bool bad = false;
-    // This warp's window candidates: rows 8 warp .. 8 warp + 7 of every window tile, read two at a time and three
-    // reads ahead, across tiles. (Straight code for all eight rows is slower: a warp cannot fetch it fast enough.)
-    auto window_row = [&](int u) -> int { return (u >> 3) * kWinRows + 8 * warp + (u & 7); };
-    RowPair w0, w1, w2;
-    auto window_read = [&](RowPair& w, int u) {
+    // This warp's window candidates: rows 16 half + 4 warp .. + 3 of every window tile, read a window tile ahead.
+    RowPair wr[2];
+    auto window_read = [&](int w) {
+      const int k0 = w * kWinRows + 16 * half + 4 * warp;
+      int slot = (p0 + (k0 < nwin ? k0 : 0)) % P.ring_cap;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int k = window_row(u + i);
-        read_row(w, i, ring + (long long)((p0 + (k < nwin ? k : 0)) % P.ring_cap) * 512, k < nwin);
+      for (int i = 0; i < 4; ++i) {
+        read_row(wr[i >> 1], i & 1, ring + (long long)slot * 512, k0 + i < nwin);
+        slot = slot + 1 == P.ring_cap ? 0 : slot + 1;
       }
     };
-    // Window tile w into `stage`: candidate r of the tile in rows r and r + 32.
+    // Window tile w into `stage` of both CTAs: candidate r of the tile in rows r and r + 32.
     auto window_store = [&](int w, int stage) {
       uint8_t* st = stages + (size_t)stage * kStage;
-#pragma unroll 1
-      for (int u = 8 * w; u < 8 * w + 8; u += 2) {
+      const uint32_t st_peer = mapa_shared(smem_u32(st), peer), sc_peer = mapa_shared(smem_u32(&sm.scale[stage][0]), peer),
+                     bar = mapa_shared(smem_u32(&sm.wr_full[stage]), peer);
+      if (pt == 0) mbar_arrive_expect_tx(&sm.wr_full[stage], kPeerTile);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = 8 * warp + (u & 7) + i;
-          RowPieces pc;
-          const float s = split_row<false>(w0.a[i], w0.c[i], pc);
-          store_codes(st, kBlk, r, lane, pc.hi);
-          store_codes(st, kBlk, r + kWinRows, lane, pc.lo);
-          if (lane == 0) sm.scale[stage][r] = sm.scale[stage][r + kWinRows] = (w * kWinRows + r < nwin) ? s : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        const int r = 16 * half + 4 * warp + i;
+        RowPieces pc;
+        float s = split_row<false>(wr[i >> 1].a[i & 1], wr[i >> 1].c[i & 1], pc);
+        store_codes(st, st_peer, bar, kBlk, r, lane, pc.hi);
+        store_codes(st, st_peer, bar, kBlk, r + kWinRows, lane, pc.lo);
+        if (w * kWinRows + r >= nwin) s = 0.f;
+        if (lane < 2) {
+          sm.scale[stage][r + kWinRows * lane] = s;
+          st_async_b32(sc_peer + 4 * (r + kWinRows * lane), __float_as_uint(s), bar);
         }
-        w0 = w1;
-        w1 = w2;
-        window_read(w2, u + 6);
       }
       fence_proxy_async_smem();
       mbar_arrive(&sm.kv_full[stage]);
     };
-    auto window_begin = [&](int w) {
-      window_read(w0, 8 * w);
-      window_read(w1, 8 * w + 2);
-      window_read(w2, 8 * w + 4);
-    };
+
     // Number of candidates: up to the last valid place of the list (-1 in between is a masked row), or every entry.
-    int n = ecap;
+    // The entries of the first two tiles are read with the list, before the count is known.
+    const int lk = warp + 4 * (lane & 15);  // the row of a tile that lane i < 16 looks after
+    int n = ecap, e0 = lk, e1 = lk + kRows;
     if (sel != nullptr) {
+      e0 = lk < P.topk ? sel[lk] : -1;
+      e1 = lk + kRows < P.topk ? sel[lk + kRows] : -1;
       int last = 0;
       for (int j = pt; j < P.topk; j += kProd)
         if (sel[j] >= 0) last = j + 1;
@@ -354,18 +372,10 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
       sm.entry_tiles = Te;
       mbar_arrive(&sm.list_ready);
     }
-    // The first window tile of this CTA is read now, each next one as the one before is stored.
-    {
-      bool win = false;
-      int w = 0;
-      for (int j = 0; j < J && !win; ++j) w = tile_of(tile0 + j, Tw, Te, win);
-      if (win) window_begin(w);
-    }
-
     // Lane i < 16 of a warp has the tile's row warp + 4 i: its entry is read two tiles ahead, its page one tile ahead.
     auto entry_of = [&](int j) -> int {
       bool win;
-      const int k = tile_of(tile0 + j, Tw, Te, win) * kRows + warp + 4 * (lane & 15);
+      const int k = tile_of(tile0 + j, Tw, Te, win) * kRows + lk;
       if (j >= J || win || k >= n) return -1;
       return sel != nullptr ? sel[k] : k;
     };
@@ -382,21 +392,37 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
       }
       return (pg << P.page_shift) | (e & ((1 << P.page_shift) - 1));
     };
-    int next_entry = entry_of(1), next_row = pool_row(entry_of(0));
+    if (tile0 > 0 || Te < 2) {  // (with two entry tiles or more, a query's first two tiles are these)
+      e0 = entry_of(0);
+      e1 = entry_of(1);
+    } else {
+      if (lk >= n) e0 = -1;
+      if (lk + kRows >= n || J < 2) e1 = -1;
+    }
+    int next_row = pool_row(e0), next_entry = e1;
+    // The first window tile of this CTA is read now, each next one as the one before is stored.
+    {
+      bool win = false;
+      int w = 0;
+      for (int j = 0; j < J && !win; ++j) w = tile_of(tile0 + j, Tw, Te, win);
+      if (win) window_read(w);
+    }
+
     for (int j = 0; j < J; ++j) {
       const int stage = j & (kStages8 - 1);
       const int my_row = next_row;
       next_row = pool_row(next_entry);
       next_entry = entry_of(j + 2);
       if (j >= kStages8) {
-        if (!mbar_wait(&sm.kv_free[stage], (uint32_t)((j / kStages8 - 1) & 1), abort_flag, status, 302)) break;
+        if (!mbar_wait_cluster(&sm.kv_free[stage], (uint32_t)((j / kStages8 - 1) & 1), abort_flag, status, 302)) break;
       } else if (j >= 2) {
-        if (!mbar_wait(&sm.q_done, 0, abort_flag, status, 301)) break;
+        if (!mbar_wait_cluster(&sm.q_done, 0, abort_flag, status, 301)) break;
       }
       bool win;
       const int index = tile_of(tile0 + j, Tw, Te, win);
       if (win) {
         window_store(index, stage);
+        if (index + 1 < Tw) window_read(index + 1);
         continue;
       }
       const uint32_t st = smem_u32(stages + (size_t)stage * kStage) + (uint32_t)(lane >> 3) * kBlk;
@@ -411,6 +437,9 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
                          my_row >= 0);
       cp_async_arrive_noinc(&sm.kv_full[stage]);
     }
+    // The other CTA's last commits have arrived here too (this CTA's shared memory may be given up after the end).
+    for (int j = max(0, J - kStages8); j < J; ++j)
+      if (!mbar_wait_cluster(&sm.kv_free[j & (kStages8 - 1)], (uint32_t)((j / kStages8) & 1), abort_flag, status, 303)) break;
     cp_async_wait_all();  // after an abort: let the copies land before teardown
     if (bad && half == 0) record_status(status, CSA_DEV_BOUNDS);
   } else if (warp == kQkWarp) {
@@ -418,15 +447,24 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
     // The whole warp walks the loop, so that addresses and descriptors stay in uniform registers (a thread by
     // itself in a divergent branch took 80 cycles to issue each MMA of 47); one thread issues.
     const bool leader = elect_one();
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_done, 0, abort_flag, status, 311)) &&
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sm.q_ready, 0, abort_flag, status, 310)) &&
+                    __all_sync(0xffffffffu, mbar_wait_cluster(&sm.q_done, 0, abort_flag, status, 311)) &&
                     __all_sync(0xffffffffu, mbar_wait(&sm.list_ready, 0, abort_flag, status, 312));
     const int J = ok ? sm.n_tiles : 0;
+    const int tile0 = sm.tile0, Te = sm.entry_tiles;
+    uint32_t wr_phase = 0;  // bit s: parity of stage s's next window tile
     constexpr uint32_t idesc1 = idesc_fp8_f32(kE4M3, kE4M3, 128, kRows, 0, 0);
     constexpr uint32_t idesc2 = idesc_fp8_f32(kE5M2, kE4M3, 128, kRows, 0, 0);
     const uint64_t dk = smem_desc_sw128(smem_u32(stages), 16, 1024), dq = smem_desc_sw128(smem_u32(q2), 16, 1024);
     for (int j = 0; j < J; ++j) {
       const int stage = j & (kStages8 - 1);
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[stage], (uint32_t)((j / kStages8) & 1), abort_flag, status, 314))) break;
+      bool win;
+      tile_of(tile0 + j, Tw, Te, win);
+      if (win) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.wr_full[stage], (wr_phase >> stage) & 1u, abort_flag, status, 316))) break;
+        wr_phase ^= 1u << stage;
+      }
       if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.s_free, (uint32_t)((j - 1) & 1), abort_flag, status, 313))) break;
       fence_proxy_async_smem();  // rows written by cp.async before the MMAs read them
       tc_fence_after();
@@ -467,7 +505,7 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
           for (int ks = 0; ks < 2; ++ks)
             mma8_ts(tmem + kOCol, tmem + kPCol + 32 * g + 16 * part + 8 * ks, db + ((ks * 4096) >> 4), idesc[part],
                     (j > 0 || part > 0 || ks > 0) ? 1u : 0u);
-        mma_commit(&sm.kv_free[stage]);
+        mma_commit_cluster(&sm.kv_free[stage], 3);
         mma_commit(&sm.pv_done[j & 3]);
       }
       __syncwarp();
@@ -483,33 +521,31 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
     const int quad = warp & 3;                 // TMEM lane quadrant
     const int h = quad * 32 + lane;            // head = TMEM lane
     const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
-    // q rows 16 sw .. 16 sw + 15, two at a time and three reads ahead.
+    // q rows 64 half + 8 sw .. + 7.
     {
-      RowPair w[3];
-      auto q_read = [&](RowPair& r2, int r) {
+      const int row0 = 64 * half + 8 * sw;
+      const uint32_t q1_peer = mapa_shared(smem_u32(q1s), peer), q2_peer = mapa_shared(smem_u32(q2), peer),
+                     qf_peer = mapa_shared(smem_u32(&sm.qf[0]), peer), bar = mapa_shared(smem_u32(&sm.q_ready), peer);
+      if (sw == 0 && lane == 0) mbar_arrive_expect_tx(&sm.q_ready, kPeerQ);
+      RowPair w[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          read_row(r2, i, P.q + ((long long)qi * P.H + (r + i)) * 512, r + i < P.H && r < 16 * sw + 16);
-      };
+      for (int i = 0; i < 8; ++i)
+        read_row(w[i >> 1], i & 1, P.q + ((long long)qi * P.H + (row0 + i)) * 512, row0 + i < P.H);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) q_read(w[i], 16 * sw + 2 * i);
-#pragma unroll 1
-      for (int r = 16 * sw; r < 16 * sw + 16; r += 2) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          RowPieces pc;
-          const float f = split_row<true>(w[0].a[i], w[0].c[i], pc);
-          store_codes(q1s, kQBlk, r + i, lane, pc.hi);
-          store_codes(q2, kQBlk, r + i, lane, pc.lo);
-          if (lane == 0) sm.qf[r + i] = f * P.scale_log2;
+      for (int i = 0; i < 8; ++i) {
+        RowPieces pc;
+        const float f = split_row<true>(w[i >> 1].a[i & 1], w[i >> 1].c[i & 1], pc) * P.scale_log2;
+        store_codes(q1s, q1_peer, bar, kQBlk, row0 + i, lane, pc.hi);
+        store_codes(q2, q2_peer, bar, kQBlk, row0 + i, lane, pc.lo);
+        if (lane == 0) {
+          sm.qf[row0 + i] = f;
+          st_async_b32(qf_peer + 4 * (row0 + i), __float_as_uint(f), bar);
         }
-        w[0] = w[1];
-        w[1] = w[2];
-        q_read(w[2], r + 6);
       }
     }
     fence_proxy_async_smem();  // q2 before the MMAs read it
-    named_bar_sync(1, 2 * kGroup);
+    mbar_arrive(&sm.q_ready);
+    bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sm.q_ready, 0, abort_flag, status, 330));
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {  // q1 -> TMEM: group g brings blocks 2 g and 2 g + 1
       const int kb = 2 * g + kk;
@@ -527,6 +563,7 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
     tmem_wait_st();
     tc_fence_before();
     mbar_arrive(&sm.q_done);
+    mbar_arrive_remote_relaxed(mapa_shared(smem_u32(&sm.q_done), peer));  // this thread has read its part of the staging area
 
     // Inverse-RoPE table for position t, while the first scores are on their way (the epilogue's barrier orders it).
     const int st = threadIdx.x - kSoftWarp * 32;  // 0..255
@@ -536,7 +573,7 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
       sm.rope_cs[st][0] = cs;
       sm.rope_cs[st][1] = -sn;
     }
-    bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.list_ready, 0, abort_flag, status, 331));
+    ok = __all_sync(0xffffffffu, mbar_wait(&sm.list_ready, 0, abort_flag, status, 331)) && ok;
     const int J = ok ? sm.n_tiles : 0;
     const int tile0 = sm.tile0, Te = sm.entry_tiles;
     const float qf = sm.qf[h];
@@ -548,6 +585,7 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
       return i < 0 || __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[i & 3], (uint32_t)((i / 4) & 1), abort_flag, status, 332));
     };
     float m_used = -CUDART_INF_F, l = 0.f;
+    uint32_t wr_phase = 0;  // bit s: parity of stage s's next window tile
     for (int j = g; j < J; j += 2) {
       const int stage = j & (kStages8 - 1);
       bool win;
@@ -557,6 +595,13 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[stage], (uint32_t)((j / kStages8) & 1), abort_flag, status, 333))) {
         ok = false;
         break;
+      }
+      if (win) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.wr_full[stage], (wr_phase >> stage) & 1u, abort_flag, status, 336))) {
+          ok = false;
+          break;
+        }
+        wr_phase ^= 1u << stage;
       }
       __syncwarp();  // the last tile's factors have been read
 #pragma unroll
@@ -734,7 +779,7 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
     if (fin) {
       const int rope0 = 512 - P.rope_dim;
       // Rows are staged in shared memory (the stages, then q2's place: every gather and MMA completed), 16 bytes apart
-      // against bank conflicts, and leave whole.
+      // against bank conflicts; each warp then sends off the rows of its quadrant, half of them, whole.
       const bool wide = P.splits > 1 || P.out_is_f32;
       const uint32_t row_bytes = wide ? 1024 : 512;
       uint8_t* srow = stages + (size_t)h * (row_bytes + 16);
@@ -760,34 +805,38 @@ __global__ void __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) 
           }
         }
         if (wide) {
-          float4* dst = reinterpret_cast<float4*>(srow + 4 * lc);
+          float4* s4 = reinterpret_cast<float4*>(srow + 4 * lc);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          for (int c = 0; c < 8; ++c) s4[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(srow + 2 * lc);
+          uint4* s4 = reinterpret_cast<uint4*>(srow + 2 * lc);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            dst[c] = make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-                                pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+            s4[c] = make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
+                               pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
         }
       }
-      // Each head row's bytes leave in one bulk store, once both groups staged their halves.
-      fence_proxy_async_smem();
       named_bar_sync(1, 2 * kGroup);
-      if (g == 0 && h < P.H) {
-        const long long at = ((long long)(P.splits > 1 ? item : qi) * P.H + h) * 512 + 256 * half;
-        void* dst = P.splits > 1 ? static_cast<void*>(P.part_o + at)
-                    : P.out_is_f32 ? static_cast<void*>(static_cast<float*>(P.out) + at)
-                                   : static_cast<void*>(static_cast<uint16_t*>(P.out) + at);
-        bulk_store_global(dst, smem_u32(srow), row_bytes);
-        bulk_commit();
-        bulk_wait_read_all();
+      const long long at = (long long)(P.splits > 1 ? item : qi) * P.H * 512 + 256 * half;
+      uint4* out = reinterpret_cast<uint4*>(P.splits > 1 ? static_cast<void*>(P.part_o) : P.out);
+      const int r0 = 32 * quad + 16 * g, r1 = min(P.H, r0 + 16);
+      if (wide) {
+        for (int r = r0; r < r1; ++r) {
+          const uint4* src = reinterpret_cast<const uint4*>(stages + (size_t)r * 1040);
+          uint4* dst = out + (at + (long long)r * 512) / 4;
+          dst[lane] = src[lane];
+          dst[32 + lane] = src[32 + lane];
+        }
+      } else {
+#pragma unroll 4
+        for (int r = r0; r < r1; ++r)
+          out[(at + (long long)r * 512) / 8 + lane] = reinterpret_cast<const uint4*>(stages + (size_t)r * 528)[lane];
       }
     }
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // no access to the other CTA's shared memory after this point
   tc_fence_after();
   if (warp == kPvWarp8) tmem_dealloc(tmem, 512);
 }

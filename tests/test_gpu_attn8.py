@@ -375,6 +375,9 @@ def test_strides_streams_and_graphs(ops):
     ws = ops.workspace(ops._lib.CSA_WS_SPARSE_ATTN, B, 1, 1, 1)
     want = ops.sparse_attn8(pos, q, ring.contiguous(), cache, idx, sink, W, ws=ws)
     assert torch.equal(ops.sparse_attn8(pos, q, ring, cache, idx, sink, W, ws=ws), want)
+    off = torch.empty(q.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(q.shape)   # 16 bytes past a multiple of 32
+    assert torch.equal(ops.sparse_attn8(pos, q, ring, cache, idx, sink, W, ws=ws[:256], out=off),
+                       ops.sparse_attn8(pos, q, ring, cache, idx, sink, W, ws=ws[:256]))
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):

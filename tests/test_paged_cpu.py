@@ -154,6 +154,10 @@ def test_bad_arguments(lib, name, bad, code):
     assert dict(calls(lib, table(), cache8(), cache16()))[name](**bad) == code
 
 
+def test_attention_without_arguments(lib):
+    assert lib.csa_sparse_attn8(None, None) == ARG and lib.hca_attn8(None, None) == ARG
+
+
 def test_bindings_refuse_host_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         ops.PageTable(torch.zeros(2, 2, dtype=torch.int32), torch.zeros(4, dtype=torch.int32), 16)

@@ -24,19 +24,22 @@
 // y_j = l_j + log2 s_j; the denominator takes P back to p_j with 1 / s_j. The sink enters at the end
 // only: it must not push P below e4m3's range.
 //
-// Layout: a cluster of two CTAs per query; CTA `half` accumulates O[:, 256 half .. 256 half + 256) (128 heads x 256
-// columns of fp32 are half of TMEM) and computes the scores over all 512 dims itself. Both CTAs so gather
-// whole rows: 512 bytes, as many as the half row of a bf16 cache, and no partial score crosses the pair.
-//   TMEM (512 columns): [0,128) q1 (four codes a column); [128,192) the scores of a 64-row tile; [192,224)
-//     and [224,256) P of even and odd tiles (p1, then p2); [256,512) O. The scores leave for registers as soon
-//     as they are there, so the score MMAs of the next tile run during the softmax of this one.
-//   SMEM: four 32 KB stages of 64 rows (four 128-byte blocks in the 128B-swizzled layout, which serves the
-//     scores as a K-major and PV as an MN-major operand); q2 (64 KB).
-//   Each CTA splits half of q's heads and half of every window tile's rows and writes the pieces into both CTAs'
-//     shared memory (the splits are bound by integer and conversion rates: whole ones cost 8 us a query more).
-//   Warps: 0..3 split window rows and gather entries (16-byte cp.async, a warp covering one row an
-//     instruction); 4 issues the score MMAs, 5 the PV MMAs (and owns TMEM); 6..9 and 10..13 are the softmax groups
-//     of even and odd tiles, one head (TMEM lane) a thread; both first split q, and share the epilogue.
+// Layout: a cluster of two CTAs per query. CTA `half` accumulates O[:, 256 half .. 256 half + 256) (128 heads x 256
+// columns of fp32 are half of TMEM) over all tiles of 64 rows; the scores and the softmax of a tile are one
+// CTA's (tile j: CTA j % 2's own), which sends P (16 KB) to the other. So of a tile its owner gathers whole rows and the other
+// CTA its half of them, and the tensor cores spend 1264 cycles a tile and CTA (scores 1504 every other tile, PV 512).
+//   TMEM (512 columns): [0,128) q1 (four codes a column); [128,192) the scores of an own tile; [192,224)
+//     and [224,256) P of even and odd own tiles (p1, then p2); [256,512) O. The scores leave for registers as soon
+//     as they are there, so the score MMAs of the next own tile run during the softmax of this one.
+//   SMEM (128B-swizzled blocks of 64 rows x 128 dims, which serve the scores as a K-major and PV as an MN-major
+//     operand): six slots A of this CTA's 256 dims (a slot a tile, until its PV completed), two slots B of the other
+//     256 dims (own tiles, until their scores are there), a buffer for the other CTA's P; q2 (64 KB).
+//   Warps: 0..3 split window rows and gather entries (16-byte cp.async); 4 issues the score MMAs, 5 the PV MMAs
+//     (and owns TMEM); 6..9 and 10..13 are the softmax groups of even and odd own tiles, one head (TMEM lane)
+//     a thread; both first split q (each CTA half of the heads, for both), and share the epilogue.
+//   The reference of P and O (the maximum, when it last had to be raised) is handed from tile to tile, so across the
+//     CTAs each time: the group of tile j takes over that of tile j - 1, rescales its CTA's O if it changed, allows
+//     PV(j - 1) (ack), raises it if its own scores ask for it, and hands it on before it forms P.
 // Split-candidate mode (few queries): as in attn.cu; attn_combine_kernel merges the partials.
 
 #include <cuda_fp16.h>
@@ -60,9 +63,9 @@ constexpr int kSoftWarp = 6;                    // warps 6..9 (even tiles), 10..
 constexpr int kGroup = 128;                     // threads of a softmax group
 constexpr int kRows = 64;                       // rows of a tile
 constexpr int kWinRows = 32;                    // window candidates of a tile (two rows each)
-constexpr int kStages8 = 4;
-constexpr uint32_t kBlk = kRows * 128;          // one 128-dim block of a stage
-constexpr uint32_t kStage = 4 * kBlk;           // 32 KB
+constexpr int kA = 6;                           // slots A
+constexpr uint32_t kBlk = kRows * 128;          // a block: 64 rows x 128 dims
+constexpr uint32_t kSlot = 2 * kBlk;            // a slot: 256 dims (16 KB); a P buffer of 128 heads x (p1, p2) is as large
 constexpr uint32_t kQBlk = 128 * 128;           // one 128-dim block of a q piece
 constexpr uint32_t kQ2Bytes = 4 * kQBlk;        // 64 KB
 // TMEM columns.
@@ -73,31 +76,37 @@ constexpr float kHead = 4.25f, kOver = 0.75f;
 static_assert(kAttn8Threads == 32 * (kSoftWarp + 8), "warp roles");
 
 struct Smem8 {
-  uint64_t kv_full[kStages8];  // this CTA's rows of the stage are there
-  uint64_t wr_full[kStages8];  // ... and the other CTA's, for a window tile
-  uint64_t kv_free[kStages8];  // PV of the stage's tile completed in both CTAs
-  uint64_t s_full[2];      // the scores of tile j are written (barrier j % 2: a group looks at its own tiles only)
-  uint64_t s_free;         // ... and have left for registers (phase j)
-  uint64_t p_full[2];      // P of tile j stored (P buffer j % 2)
-  uint64_t pv_done[4];     // PV(j) completed (barrier j % 4): its P buffer is free, O holds PV(0..j)
+  uint64_t a_full[kA];     // this CTA's producers are done with the tile (for the other CTA's window tile: nothing to do)
+  uint64_t w_full[kA];     // rows of a window tile that the other CTA owns
+  uint64_t a_free[kA];     // PV of the slot's tile completed in both CTAs
+  uint64_t b_free[2];      // the scores of own tile i are there: slot B i % 2 is free
+  uint64_t s_full[2];      // the same, for the softmax (barrier i % 2: a group looks at its own tiles only)
+  uint64_t s_free;         // ... and have left for registers (phase i)
+  uint64_t p_full[2];      // P of own tile i stored (TMEM buffer i % 2)
+  uint64_t pb_full[2];     // P of the other CTA's own tile i (i % 2) arrived
+  uint64_t pb_free[2];     // PV of own tile i (i % 2) completed in the other CTA: its P buffer is free
+  uint64_t ack[2];         // group g took over the reference of the other CTA's tile: O is ready for its PV
+  uint64_t pv_done[4];     // PV(j) completed (barrier j % 4): O holds PV(0..j)
+  uint64_t hand[2][4];     // the reference after the other CTA's tile of its group g (quadrant q) arrived
+  uint64_t ex_full;        // the other CTA's denominators
   uint64_t q_ready;        // both CTAs' pieces of q are in shared memory
-  uint64_t q_done;         // q1 is in TMEM in both CTAs: the staging area (stages 2, 3) is free
+  uint64_t q_done;         // q1 is in TMEM in both CTAs: the staging area (slots A 3 to 5, the P buffer) is free
   uint64_t list_ready;
-  uint64_t hand[2][4];     // softmax group g published the running maximum after its tile (quadrant q)
   uint64_t drain[2];
   uint32_t tmem_base;
-  int abort_flag, bad, epi_bad;
+  int abort_flag, epi_bad;
   int n_tiles, tile0, entry_tiles;
   int last[kProd / 32];
   float rope_cs[kMaxRopePairs][2];
   float qf[128];           // per head: 2^k_h * scale * log2(e)
-  float m_hand[4][32];
-  float l_g[2][128], m_g[2][128];
-  float scale[kStages8][kRows];                       // the rows' scales, as gathered
+  float2 hand_m[2][128];   // (the reference before that tile, after it)
+  float l_g[4][128], m_g[4][128];                     // of this CTA's groups, then of the other's
+  float scale[4][kRows];                              // scales of own tile i's rows (i % 4), as gathered
   alignas(16) float col_a[8][kRows], col_k[8][kRows], col_i[8][kRows];  // (read four at a time) per softmax warp: s_j, log2 s_j, 1 / s_j of its tile's columns
 };
 
-static_assert(128 * (1024 + 16) <= kStages8 * kStage + kQ2Bytes, "output staging");
+constexpr size_t kTileBytes = (kA + 3) * (size_t)kSlot;  // slots A, P buffer, slots B
+static_assert(128 * (1024 + 16) <= kTileBytes + kQ2Bytes, "output staging");
 static_assert(offsetof(Smem8, col_a) % 16 == 0 && sizeof(Smem8::col_a[0]) % 16 == 0, "float4 reads of the column factors");
 
 // The upper bytes of two fp16 pairs (their e5m2 codes, the lower bits dropped).
@@ -168,17 +177,17 @@ __device__ __forceinline__ float split_row(const uint4& a, const uint4& b, RowPi
   return e < 255 ? __uint_as_float((uint32_t)(127 + k) << 23) : CUDART_NAN_F;
 }
 
-// What a CTA gets from the other: of a window tile (16 rows, two pieces and two scales each), and of q (64 heads, two
-// pieces and a factor each).
-constexpr uint32_t kPeerTile = 16 * (2 * 512 + 2 * 4), kPeerQ = 64 * (2 * 512 + 4);
+// Bytes that a CTA gets from the other: of a window tile (two pieces of 32 half rows), of q (64 heads, two pieces and a
+// factor each), of a tile's P, a warp's references, the denominators.
+constexpr uint32_t kPeerTile = 2 * 32 * 256, kPeerQ = 64 * (2 * 512 + 4), kPeerP = 128 * 128, kPeerRef = 32 * 8, kPeerSum = 2 * 128 * 8;
 
-// Store lane l's 8 + 8 codes of row `row` into a [4 blocks][rows][128 B] swizzled region of block size `blk`: of this
-// CTA (at `base`) and of the other (at cluster address `peer`, the bytes counted on its barrier `bar`).
-__device__ __forceinline__ void store_codes(uint8_t* base, uint32_t peer, uint32_t bar, uint32_t blk, int row, int lane, const uint2 (&v)[2]) {
+// Store lane l's 8 + 8 codes of head `row` into a [4 blocks][128 rows][128 B] swizzled region: of this CTA (at `base`)
+// and of the other (at cluster address `peer`, the bytes counted on its barrier `bar`).
+__device__ __forceinline__ void store_q(uint8_t* base, uint32_t peer, uint32_t bar, int row, int lane, const uint2 (&v)[2]) {
   const uint32_t off = sw128_offset((uint32_t)row, (uint32_t)((lane & 15) >> 1)) + (uint32_t)(lane & 1) * 8u;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t at = (uint32_t)(2 * i + (lane >> 4)) * blk + off;
+    const uint32_t at = (uint32_t)(2 * i + (lane >> 4)) * kQBlk + off;
     *reinterpret_cast<uint2*>(base + at) = v[i];
     st_async_v2(peer + at, v[i].x, v[i].y, bar);
   }
@@ -206,19 +215,21 @@ __device__ __forceinline__ void split_p(float p0, float p1, float p2, float p3, 
   c2 = codes_e5m2(rest2(h0, a0) + 0x00800080u, rest2(h1, a1) + 0x00800080u);
 }
 
-// Order of a query's tiles: up to two entry tiles first, whose gathers are quick, then window and entry tiles in turn while
-// both last: the split of a window tile takes the gathering warps longer than the tensor cores need for a tile.
-// (It also spreads the window over the splits of a query.) Returns the index of tile p among those of its kind.
+// Order of a query's tiles: two entry tiles first, whose gathers are quick, then pairs of window and of entry tiles in turn while
+// both last, the rest of the window, the rest of the entries: the split of a window tile takes the gathering warps longer than
+// the tensor cores need for a tile. (Pairs, so that each CTA owns half of the window; and it spreads the window
+// over the splits of a query.) Returns the index of tile p among those of its kind.
 __device__ __forceinline__ int tile_of(int p, int Tw, int Te, bool& win) {
-  const int e0 = min(Te, 2), both = min(Tw, Te - e0), q = p - e0;
+  const int alt = Te < 2 ? 0 : min(Tw >> 1, (Te - 2) >> 1), e0 = Te < 2 ? 0 : 2, q = p - e0;
   win = false;
   if (q < 0) return p;
-  if (q < 2 * both) {
-    win = (q & 1) == 0;
-    return win ? q >> 1 : e0 + (q >> 1);
+  if (q < 4 * alt) {
+    win = (q & 2) == 0;
+    return (q >> 2) * 2 + (q & 1) + (win ? 0 : e0);
   }
-  win = Tw > both;
-  return win ? q - both : p - both;
+  const int r = q - 4 * alt, w = 2 * alt + r;  // the first of what is left is window tile 2 alt
+  win = w < Tw;
+  return win ? w : e0 + 2 * alt + (w - Tw);
 }
 
 // Two fp32 operations an instruction.
@@ -251,9 +262,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) attn8_kernel(Attn8Params P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* stages = base;
-  uint8_t* q2 = base + kStages8 * kStage;
-  uint8_t* q1s = stages + 2 * kStage;            // q1 on its way to TMEM: stages 2 and 3
+  uint8_t* slots_a = base;
+  uint8_t* pb = slots_a + kA * kSlot;
+  uint8_t* slots_b = pb + kSlot;
+  uint8_t* q2 = base + kTileBytes;
+  uint8_t* q1s = slots_a + 3 * kSlot;            // q1 on its way to TMEM: slots A 3 to 5, the P buffer
   Smem8& sm = *reinterpret_cast<Smem8*>(q2 + kQ2Bytes);
 
   const int warp = warp_id(), lane = lane_id();
@@ -266,24 +279,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
   uint32_t* status = P.status;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages8; ++i) {
-      mbar_init(&sm.kv_full[i], kProd);
-      mbar_init(&sm.wr_full[i], 1);
-      mbar_init(&sm.kv_free[i], 2);
+    for (int i = 0; i < kA; ++i) {
+      mbar_init(&sm.a_full[i], kProd);
+      mbar_init(&sm.w_full[i], 1);
+      mbar_init(&sm.a_free[i], 2);
     }
     mbar_init(&sm.s_free, kGroup);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.b_free[i], 1);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], kGroup);
-      for (int q = 0; q < 4; ++q) mbar_init(&sm.hand[i][q], 32);
+      mbar_init(&sm.pb_full[i], 1);
+      mbar_init(&sm.pb_free[i], 1);
+      mbar_init(&sm.ack[i], kGroup);
+      for (int q = 0; q < 4; ++q) mbar_init(&sm.hand[i][q], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&sm.pv_done[i], 1);
+    mbar_init(&sm.ex_full, 1);
     mbar_init(&sm.q_ready, 2 * kGroup + 1);
     mbar_init(&sm.q_done, 4 * kGroup);
     mbar_init(&sm.list_ready, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.drain[i], 1);
     sm.abort_flag = 0;
-    sm.bad = 0;
     sm.epi_bad = 0;
     fence_mbar_init();
   }
@@ -304,6 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
   const int p0 = t - nwin + 1;
   const int Tw = (nwin + kWinRows - 1) / kWinRows;
   const int ecap = t < 0 ? 0 : min((int)(((long long)t + 1) / P.ratio), P.max_entries);
+  // Tile j (of this item's J) is CTA j % 2's own, the (j >> 1)-th of them; it lies in slot A j % kA.
 
   if (warp < kProd / 32) {
     // ------------------------------------------------------------ window split, gathers
@@ -312,38 +330,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
     const uint16_t* ring = P.ring + (long long)b * P.ring_bstride;
     const int32_t* sel = P.topk_idx == nullptr ? nullptr : P.topk_idx + (long long)qi * P.topk;
     bool bad = false;
-    // This warp's window candidates: rows 16 half + 4 warp .. + 3 of every window tile, read a window tile ahead.
-    RowPair wr[2];
+    // This warp's candidates of window tile w: rows 8 warp .. + 7, read an own window tile ahead.
+    RowPair wr[4];
     auto window_read = [&](int w) {
-      const int k0 = w * kWinRows + 16 * half + 4 * warp;
+      const int k0 = w * kWinRows + 8 * warp;
       int slot = (p0 + (k0 < nwin ? k0 : 0)) % P.ring_cap;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         read_row(wr[i >> 1], i & 1, ring + (long long)slot * 512, k0 + i < nwin);
         slot = slot + 1 == P.ring_cap ? 0 : slot + 1;
       }
     };
-    // Window tile w into `stage` of both CTAs: candidate r of the tile in rows r and r + 32.
-    auto window_store = [&](int w, int stage) {
-      uint8_t* st = stages + (size_t)stage * kStage;
-      const uint32_t st_peer = mapa_shared(smem_u32(st), peer), sc_peer = mapa_shared(smem_u32(&sm.scale[stage][0]), peer),
-                     bar = mapa_shared(smem_u32(&sm.wr_full[stage]), peer);
-      if (pt == 0) mbar_arrive_expect_tx(&sm.wr_full[stage], kPeerTile);
+    // Own window tile w, own tile i: candidate r in rows r and r + 32 of slots A `slot` and B i % 2, and of the other
+    // CTA's slot A (its half of the dims).
+    auto window_store = [&](int w, int slot, int i0) {
+      uint8_t* mine = slots_a + (size_t)slot * kSlot;
+      uint8_t* other = slots_b + (size_t)(i0 & 1) * kSlot;
+      const uint32_t far = mapa_shared(smem_u32(mine), peer), bar = mapa_shared(smem_u32(&sm.w_full[slot]), peer);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 16 * half + 4 * warp + i;
+      for (int i = 0; i < 8; ++i) {
+        const int r = 8 * warp + i;
         RowPieces pc;
         float s = split_row<false>(wr[i >> 1].a[i & 1], wr[i >> 1].c[i & 1], pc);
-        store_codes(st, st_peer, bar, kBlk, r, lane, pc.hi);
-        store_codes(st, st_peer, bar, kBlk, r + kWinRows, lane, pc.lo);
-        if (w * kWinRows + r >= nwin) s = 0.f;
-        if (lane < 2) {
-          sm.scale[stage][r + kWinRows * lane] = s;
-          st_async_b32(sc_peer + 4 * (r + kWinRows * lane), __float_as_uint(s), bar);
+#pragma unroll
+        for (int lo = 0; lo < 2; ++lo) {
+          const uint2 v0 = lo ? pc.lo[0] : pc.hi[0], v1 = lo ? pc.lo[1] : pc.hi[1];
+          const uint2 a = half ? v1 : v0, c = half ? v0 : v1;
+          const uint32_t off = (uint32_t)(lane >> 4) * kBlk + sw128_offset((uint32_t)(r + kWinRows * lo), (uint32_t)((lane & 15) >> 1)) +
+                               (uint32_t)(lane & 1) * 8u;
+          *reinterpret_cast<uint2*>(mine + off) = a;
+          *reinterpret_cast<uint2*>(other + off) = c;
+          st_async_v2(far + off, c.x, c.y, bar);
         }
+        if (w * kWinRows + r >= nwin) s = 0.f;
+        if (lane < 2) sm.scale[i0 & 3][r + kWinRows * lane] = s;
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sm.kv_full[stage]);
+      mbar_arrive(&sm.a_full[slot]);
     };
 
     // Number of candidates: up to the last valid place of the list (-1 in between is a masked row), or every entry.
@@ -372,6 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       sm.entry_tiles = Te;
       mbar_arrive(&sm.list_ready);
     }
+
     // Lane i < 16 of a warp has the tile's row warp + 4 i: its entry is read two tiles ahead, its page one tile ahead.
     auto entry_of = [&](int j) -> int {
       bool win;
@@ -396,54 +420,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       e0 = entry_of(0);
       e1 = entry_of(1);
     } else {
-      if (lk >= n) e0 = -1;
+      if (lk >= n || J < 1) e0 = -1;
       if (lk + kRows >= n || J < 2) e1 = -1;
     }
     int next_row = pool_row(e0), next_entry = e1;
-    // The first window tile of this CTA is read now, each next one as the one before is stored.
+    // The first own window tile is read now, each next one as the one before is stored.
     {
       bool win = false;
       int w = 0;
-      for (int j = 0; j < J && !win; ++j) w = tile_of(tile0 + j, Tw, Te, win);
+      for (int j = half; j < J && !win; j += 2) w = tile_of(tile0 + j, Tw, Te, win);
       if (win) window_read(w);
     }
-
+    int slot = 0;
+    uint32_t ph = 0;
     for (int j = 0; j < J; ++j) {
-      const int stage = j & (kStages8 - 1);
       const int my_row = next_row;
       next_row = pool_row(next_entry);
       next_entry = entry_of(j + 2);
-      if (j >= kStages8) {
-        if (!mbar_wait_cluster(&sm.kv_free[stage], (uint32_t)((j / kStages8 - 1) & 1), abort_flag, status, 302)) break;
-      } else if (j >= 2) {
+      if (j >= kA) {
+        if (!mbar_wait_cluster(&sm.a_free[slot], ph ^ 1u, abort_flag, status, 302)) break;
+      } else if (j >= 3) {
         if (!mbar_wait_cluster(&sm.q_done, 0, abort_flag, status, 301)) break;
       }
       bool win;
-      const int index = tile_of(tile0 + j, Tw, Te, win);
-      if (win) {
-        window_store(index, stage);
-        if (index + 1 < Tw) window_read(index + 1);
-        continue;
-      }
-      const uint32_t st = smem_u32(stages + (size_t)stage * kStage) + (uint32_t)(lane >> 3) * kBlk;
+      const int index = tile_of(tile0 + j, Tw, Te, win), i0 = j >> 1;
+      const uint32_t sa = smem_u32(slots_a + (size_t)slot * kSlot);
+      if ((j & 1) == half) {
+        if (i0 >= 2 && !mbar_wait(&sm.b_free[i0 & 1], (uint32_t)((i0 >> 1) & 1) ^ 1u, abort_flag, status, 304)) break;
+        if (win) {
+          window_store(index, slot, i0);
+          if (index + 2 < Tw) window_read(index + 2);
+        } else {
+          const uint32_t sb = smem_u32(slots_b + (size_t)(i0 & 1) * kSlot);
+          const uint32_t st = ((lane >> 4) == half ? sa : sb) + (uint32_t)((lane >> 3) & 1) * kBlk;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int row = __shfl_sync(0xffffffffu, my_row, i);
-        cp_async_16_zfill(st + sw128_offset((uint32_t)(warp + 4 * i), (uint32_t)(lane & 7)),
-                          P.pages + (long long)max(row, 0) * 512 + lane * 16, row >= 0);
+          for (int i = 0; i < 16; ++i) {
+            const int row = __shfl_sync(0xffffffffu, my_row, i);
+            cp_async_16_zfill(st + sw128_offset((uint32_t)(warp + 4 * i), (uint32_t)(lane & 7)),
+                              P.pages + (long long)max(row, 0) * 512 + lane * 16, row >= 0);
+          }
+          if (lane < 16)
+            cp_async_4_zfill(smem_u32(&sm.scale[i0 & 3][warp + 4 * lane]), P.scales + (max(my_row, 0) >> P.block_shift),
+                             my_row >= 0);
+          cp_async_arrive_noinc(&sm.a_full[slot]);
+        }
+      } else if (win) {
+        if (pt == 0) mbar_arrive_expect_tx(&sm.w_full[slot], kPeerTile);
+        mbar_arrive(&sm.a_full[slot]);
+      } else {
+        const uint32_t st = sa + (uint32_t)((lane >> 3) & 1) * kBlk;  // two half rows an instruction
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const int r = i + (lane >> 4), row = __shfl_sync(0xffffffffu, my_row, r);
+          cp_async_16_zfill(st + sw128_offset((uint32_t)(warp + 4 * r), (uint32_t)(lane & 7)),
+                            P.pages + (long long)max(row, 0) * 512 + 256 * half + (lane & 15) * 16, row >= 0);
+        }
+        cp_async_arrive_noinc(&sm.a_full[slot]);
       }
-      if (lane < 16)
-        cp_async_4_zfill(smem_u32(&sm.scale[stage][warp + 4 * lane]), P.scales + (max(my_row, 0) >> P.block_shift),
-                         my_row >= 0);
-      cp_async_arrive_noinc(&sm.kv_full[stage]);
+      if (++slot == kA) {
+        slot = 0;
+        ph ^= 1u;
+      }
     }
     // The other CTA's last commits have arrived here too (this CTA's shared memory may be given up after the end).
-    for (int j = max(0, J - kStages8); j < J; ++j)
-      if (!mbar_wait_cluster(&sm.kv_free[j & (kStages8 - 1)], (uint32_t)((j / kStages8) & 1), abort_flag, status, 303)) break;
+    for (int j = max(0, J - kA); j < J; ++j)
+      if (!mbar_wait_cluster(&sm.a_free[j % kA], (uint32_t)((j / kA) & 1), abort_flag, status, 303)) break;
     cp_async_wait_all();  // after an abort: let the copies land before teardown
     if (bad && half == 0) record_status(status, CSA_DEV_BOUNDS);
   } else if (warp == kQkWarp) {
-    // ------------------------------------------------------------ score MMAs
+    // ------------------------------------------------------------ score MMAs of the own tiles
     // The whole warp walks the loop, so that addresses and descriptors stay in uniform registers (a thread by
     // itself in a divergent branch took 80 cycles to issue each MMA of 47); one thread issues.
     const bool leader = elect_one();
@@ -451,35 +496,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
                     __all_sync(0xffffffffu, mbar_wait_cluster(&sm.q_done, 0, abort_flag, status, 311)) &&
                     __all_sync(0xffffffffu, mbar_wait(&sm.list_ready, 0, abort_flag, status, 312));
     const int J = ok ? sm.n_tiles : 0;
-    const int tile0 = sm.tile0, Te = sm.entry_tiles;
-    uint32_t wr_phase = 0;  // bit s: parity of stage s's next window tile
     constexpr uint32_t idesc1 = idesc_fp8_f32(kE4M3, kE4M3, 128, kRows, 0, 0);
     constexpr uint32_t idesc2 = idesc_fp8_f32(kE5M2, kE4M3, 128, kRows, 0, 0);
-    const uint64_t dk = smem_desc_sw128(smem_u32(stages), 16, 1024), dq = smem_desc_sw128(smem_u32(q2), 16, 1024);
-    for (int j = 0; j < J; ++j) {
-      const int stage = j & (kStages8 - 1);
-      if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[stage], (uint32_t)((j / kStages8) & 1), abort_flag, status, 314))) break;
-      bool win;
-      tile_of(tile0 + j, Tw, Te, win);
-      if (win) {
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.wr_full[stage], (wr_phase >> stage) & 1u, abort_flag, status, 316))) break;
-        wr_phase ^= 1u << stage;
-      }
-      if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.s_free, (uint32_t)((j - 1) & 1), abort_flag, status, 313))) break;
+    const uint64_t da = smem_desc_sw128(smem_u32(slots_a), 16, 1024), db = smem_desc_sw128(smem_u32(slots_b), 16, 1024);
+    // Blocks of q: this CTA's dims first (slot A), then the other's (slot B).
+    const uint64_t dq = smem_desc_sw128(smem_u32(q2), 16, 1024);
+    const uint32_t near = 2 * (uint32_t)half, far = 2 * peer;
+    int slot = half;
+    uint32_t ph = 0;
+    for (int i = 0, j = half; j < J; ++i, j += 2) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.a_full[slot], ph, abort_flag, status, 314))) break;
+      if (i > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.s_free, (uint32_t)((i - 1) & 1), abort_flag, status, 313))) break;
       fence_proxy_async_smem();  // rows written by cp.async before the MMAs read them
       tc_fence_after();
-      const uint64_t db = dk + (uint64_t)((uint32_t)stage * (kStage >> 4));
+      const uint64_t ka = da + (uint64_t)((uint32_t)slot * (kSlot >> 4)), kb = db + (uint64_t)((uint32_t)(i & 1) * (kSlot >> 4));
       if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < 16; ++ks)
-          mma8_ts(tmem + kScoreCol, tmem + 8 * ks, db + (((ks >> 2) * kBlk + (ks & 3) * 32) >> 4), idesc1, ks > 0 ? 1u : 0u);
+        for (int ks = 0; ks < 16; ++ks) {
+          const uint32_t blk = (ks < 8 ? near : far) + ((ks >> 2) & 1);
+          mma8_ts(tmem + kScoreCol, tmem + 32 * blk + 8 * (ks & 3), (ks < 8 ? ka : kb) + ((((ks >> 2) & 1) * kBlk + (ks & 3) * 32) >> 4),
+                  idesc1, ks > 0 ? 1u : 0u);
+        }
 #pragma unroll
-        for (int ks = 0; ks < 16; ++ks)
-          mma8_ss(tmem + kScoreCol, dq + (((ks >> 2) * kQBlk + (ks & 3) * 32) >> 4),
-                  db + (((ks >> 2) * kBlk + (ks & 3) * 32) >> 4), idesc2, 1u);
-        mma_commit(&sm.s_full[j & 1]);
+        for (int ks = 0; ks < 16; ++ks) {
+          const uint32_t blk = (ks < 8 ? near : far) + ((ks >> 2) & 1);
+          mma8_ss(tmem + kScoreCol, dq + ((blk * kQBlk + (ks & 3) * 32) >> 4),
+                  (ks < 8 ? ka : kb) + ((((ks >> 2) & 1) * kBlk + (ks & 3) * 32) >> 4), idesc2, 1u);
+        }
+        mma_commit(&sm.s_full[i & 1]);
+        mma_commit(&sm.b_free[i & 1]);
       }
       __syncwarp();
+      slot += 2;
+      if (slot >= kA) {
+        slot -= kA;
+        ph ^= 1u;
+      }
     }
     // Every MMA issued above completes on its own; wait for them before TMEM is released.
     if (leader) {
@@ -487,28 +539,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       mbar_wait_drain(&sm.drain[0], 0, status, 315);
     }
   } else if (warp == kPvWarp8) {
-    // ------------------------------------------------------------ PV MMAs
+    // ------------------------------------------------------------ PV MMAs of every tile
     const bool leader = elect_one();
     const int J = __all_sync(0xffffffffu, mbar_wait(&sm.list_ready, 0, abort_flag, status, 321)) ? sm.n_tiles : 0;
+    const int tile0 = sm.tile0, Te = sm.entry_tiles;
     constexpr uint32_t idesc[2] = {idesc_fp8_f32(kE4M3, kE4M3, 128, 256, 0, 1), idesc_fp8_f32(kE5M2, kE4M3, 128, 256, 0, 1)};
-    const uint64_t dv = smem_desc_sw128(smem_u32(stages) + (uint32_t)half * 2 * kBlk, kBlk, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_u32(slots_a), kBlk, 1024), dp = smem_desc_sw128(smem_u32(pb), 16, 1024);
+    int slot = 0;
+    uint32_t ph = 0, w_phase = 0;  // bit s of w_phase: parity of slot s's next window tile of the other CTA
     for (int j = 0; j < J; ++j) {
-      const int stage = j & (kStages8 - 1), g = j & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&sm.p_full[g], (uint32_t)((j / 2) & 1), abort_flag, status, 322))) break;
+      const int i = j >> 1, g = i & 1;
+      const uint32_t phase = (uint32_t)((i >> 1) & 1);
+      const bool own = (j & 1) == half;
+      if (own) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.p_full[g], phase, abort_flag, status, 322))) break;
+      } else {
+        bool win;
+        tile_of(tile0 + j, Tw, Te, win);
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.a_full[slot], ph, abort_flag, status, 324))) break;
+        if (win) {
+          if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.w_full[slot], (w_phase >> slot) & 1u, abort_flag, status, 325))) break;
+          w_phase ^= 1u << slot;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.ack[((j + 1) >> 1) & 1], (uint32_t)(((j + 1) >> 2) & 1), abort_flag, status, 326))) break;
+        if (leader) mbar_arrive_expect_tx(&sm.pb_full[g], kPeerP);
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.pb_full[g], phase, abort_flag, status, 327))) break;
+      }
       fence_proxy_async_smem();
       tc_fence_after();
-      const uint64_t db = dv + (uint64_t)((uint32_t)stage * (kStage >> 4));
+      const uint64_t vb = dv + (uint64_t)((uint32_t)slot * (kSlot >> 4));
       if (leader) {
+        if (own) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+          for (int part = 0; part < 2; ++part)
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-            mma8_ts(tmem + kOCol, tmem + kPCol + 32 * g + 16 * part + 8 * ks, db + ((ks * 4096) >> 4), idesc[part],
-                    (j > 0 || part > 0 || ks > 0) ? 1u : 0u);
-        mma_commit_cluster(&sm.kv_free[stage], 3);
+            for (int ks = 0; ks < 2; ++ks)
+              mma8_ts(tmem + kOCol, tmem + kPCol + 32 * g + 16 * part + 8 * ks, vb + ((ks * 4096) >> 4), idesc[part],
+                      (j > 0 || part > 0 || ks > 0) ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+              mma8_ss(tmem + kOCol, dp + ((64 * part + 32 * ks) >> 4), vb + ((ks * 4096) >> 4), idesc[part],
+                      (j > 0 || part > 0 || ks > 0) ? 1u : 0u);
+          mma_commit_cluster(&sm.pb_free[g], (uint16_t)(1u << peer));
+        }
+        mma_commit_cluster(&sm.a_free[slot], 3);
         mma_commit(&sm.pv_done[j & 3]);
       }
       __syncwarp();
+      if (++slot == kA) {
+        slot = 0;
+        ph ^= 1u;
+      }
     }
     if (leader) {
       mma_commit(&sm.drain[1]);
@@ -535,8 +619,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       for (int i = 0; i < 8; ++i) {
         RowPieces pc;
         const float f = split_row<true>(w[i >> 1].a[i & 1], w[i >> 1].c[i & 1], pc) * P.scale_log2;
-        store_codes(q1s, q1_peer, bar, kQBlk, row0 + i, lane, pc.hi);
-        store_codes(q2, q2_peer, bar, kQBlk, row0 + i, lane, pc.lo);
+        store_q(q1s, q1_peer, bar, row0 + i, lane, pc.hi);
+        store_q(q2, q2_peer, bar, row0 + i, lane, pc.lo);
         if (lane == 0) {
           sm.qf[row0 + i] = f;
           st_async_b32(qf_peer + 4 * (row0 + i), __float_as_uint(f), bar);
@@ -579,41 +663,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
     const float qf = sm.qf[h];
     const uint64_t qf2 = pack2(qf, qf);
     // pv_done[i % 4] completes once per PV(i). A wait for PV(i) by parity is unambiguous while PV(i - 4) is known to have
-    // completed and PV(i + 4) cannot have. A group waits for PV(j - 2) before it stores P(j), and publishes its maximum of
-    // tile j after that of tile j - 2: so whoever holds the maximum of tile j - 1 knows that PV(j - 5) completed.
+    // completed and PV(i + 4) cannot have. A group waits for PV(j - 4) first of all at tile j (its P buffer's last
+    // reader), and PVs complete in order; PV(j) needs this group's P, PV(j + 1) the reference that it hands on.
     auto wait_pv = [&](int i) -> bool {
       return i < 0 || __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[i & 3], (uint32_t)((i / 4) & 1), abort_flag, status, 332));
     };
     float m_used = -CUDART_INF_F, l = 0.f;
-    uint32_t wr_phase = 0;  // bit s: parity of stage s's next window tile
-    for (int j = g; j < J; j += 2) {
-      const int stage = j & (kStages8 - 1);
+    // O from reference m0 to m (in the lanes where that is larger).
+    auto rescale = [&](float m0, float m) {
+      const float alpha = m > m0 ? exp2f(m0 - m) : 1.f;
+      const uint64_t alpha2 = pack2(alpha, alpha);
+      tc_fence_after();
+#pragma unroll 1
+      for (int cc = 0; cc < 8; ++cc) {
+        uint32_t o[32];
+        const uint32_t oa = tmem + lane_addr + kOCol + 32 * cc;
+        tmem_ld32(oa, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float a0, a1;
+          unpack2(mul2(pack2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), alpha2), a0, a1);
+          o[e] = __float_as_uint(a0);
+          o[e + 1] = __float_as_uint(a1);
+        }
+        tmem_st32(oa, o);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+    };
+    // This group's sum from reference m_used to m.
+    auto refer_to = [&](float m) {
+      if (m > m_used) {
+        l = l != 0.f ? l * exp2f(m_used - m) : 0.f;
+        m_used = m;
+      }
+    };
+    // Take over the reference after tile j - 1, the other CTA's, and allow its PV here.
+    auto take_over = [&](int j) -> bool {
+      const int from = ((j - 1) >> 1) & 1;
+      if (lane == 0) mbar_arrive_expect_tx(&sm.hand[from][quad], kPeerRef);
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.hand[from][quad], (uint32_t)(((j - 1) >> 2) & 1), abort_flag, status, 335)))
+        return false;
+      const float2 mp = sm.hand_m[from][h];
+      if (j >= 2 && __any_sync(0xffffffffu, mp.y > mp.x)) {
+        if (!wait_pv(j - 2)) return false;
+        rescale(mp.x, mp.y);
+      }
+      refer_to(mp.y);
+      mbar_arrive(&sm.ack[g]);
+      return true;
+    };
+    const uint32_t hand_peer = mapa_shared(smem_u32(&sm.hand_m[g][h]), peer), hand_bar = mapa_shared(smem_u32(&sm.hand[g][quad]), peer),
+                   pb_peer = mapa_shared(smem_u32(pb), peer), pb_bar = mapa_shared(smem_u32(&sm.pb_full[g]), peer);
+    int last_own = -1;
+    for (int i = g, j = 2 * g + half; j < J; i += 2, j += 4) {
+      const int slot = j % kA;
       bool win;
       tile_of(tile0 + j, Tw, Te, win);
       // Column factors, two columns a lane, while the score MMAs run. A window candidate's second column
       // adds nothing to the denominator.
-      if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[stage], (uint32_t)((j / kStages8) & 1), abort_flag, status, 333))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.a_full[slot], (uint32_t)((j / kA) & 1), abort_flag, status, 333))) {
         ok = false;
         break;
       }
-      if (win) {
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.wr_full[stage], (wr_phase >> stage) & 1u, abort_flag, status, 336))) {
-          ok = false;
-          break;
-        }
-        wr_phase ^= 1u << stage;
-      }
       __syncwarp();  // the last tile's factors have been read
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = 32 * i + lane;
-        const float s = sm.scale[stage][c];
+      for (int u = 0; u < 2; ++u) {
+        const int c = 32 * u + lane;
+        const float s = sm.scale[i & 3][c];
         sm.col_a[sw][c] = s;
         sm.col_k[sw][c] = log2f(s);  // 0 (a masked column): -inf
         sm.col_i[sw][c] = (s == 0.f || (win && c >= kWinRows)) ? 0.f : 1.f / s;
       }
       __syncwarp();
-      if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[g], (uint32_t)((j / 2) & 1), abort_flag, status, 334))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[g], (uint32_t)((i >> 1) & 1), abort_flag, status, 334))) {
         ok = false;
         break;
       }
@@ -650,56 +774,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
         mx[1] = fmaxf(mx[1], fmaxf(e2, e3));
       }
       const float mt = fmaxf(mx[0], mx[1]);
-      // The running maximum after tile j - 1, from the other group (it only grows).
-      if (j > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.hand[1 - g][quad], (uint32_t)(((j - 1) / 2) & 1), abort_flag, status, 335))) {
+      if (!wait_pv(j - 4) || (j > 0 && !take_over(j))) {
+        ok = false;
+        break;
+      }
+      if (j == 0) mbar_arrive(&sm.ack[g]);  // (keeps the barrier's phases in step)
+      // Raise the reference where the scores ask for it; the TMEM accesses are warp-collective, so the warp takes
+      // the branch if any lane must.
+      const float m_before = m_used;
+      const bool need = mt > m_used + (kHead + kOver) || (m_used == -CUDART_INF_F && mt > m_used);
+      if (__any_sync(0xffffffffu, need)) {
+        if (!wait_pv(j - 1)) {
           ok = false;
           break;
         }
-        const float mp = sm.m_hand[quad][lane];
-        if (mp != m_used) {
-          l = l != 0.f ? l * exp2f(m_used - mp) : 0.f;
-          m_used = mp;
-        }
+        if (j > 0) rescale(m_before, need ? mt : m_before);
+        if (need) refer_to(mt);
       }
-      // Lazy rescale; the TMEM accesses are warp-collective, so the warp takes the branch if any lane must.
-      const bool need = mt > m_used + (kHead + kOver) || (m_used == -CUDART_INF_F && mt > m_used);
-      if (__any_sync(0xffffffffu, need)) {
-        const float alpha = need ? exp2f(m_used - mt) : 1.f;
-        if (j > 0) {
-          if (!wait_pv(j - 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t alpha2 = pack2(alpha, alpha);
-#pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {
-            uint32_t o[32];
-            const uint32_t oa = tmem + lane_addr + kOCol + 32 * cc;
-            tmem_ld32(oa, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float a0, a1;
-              unpack2(mul2(pack2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), alpha2), a0, a1);
-              o[e] = __float_as_uint(a0);
-              o[e + 1] = __float_as_uint(a1);
-            }
-            tmem_st32(oa, o);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-        }
-        if (need) {
-          l *= alpha;
-          m_used = mt;
-        }
-      }
-      if (j + 1 < J) {
-        sm.m_hand[quad][lane] = m_used;
-        mbar_arrive(&sm.hand[g][quad]);
-      }
+      st_async_v2(hand_peer, __float_as_uint(m_before), __float_as_uint(m_used), hand_bar);
       const float ref = (m_used == -CUDART_INF_F ? 0.f : m_used) + kHead;
       const uint64_t ref2 = pack2(-ref, -ref);
       uint32_t p1[16], p2[16];
@@ -723,31 +815,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
         unpack2(add2(ls[0], ls[1]), s0, s1);
         l += s0 + s1;
       }
-      if (!wait_pv(j - 2)) {  // the P buffer is free
-        ok = false;
-        break;
-      }
-      tc_fence_after();
       const uint32_t pa = tmem + lane_addr + kPCol + 32 * g;
       tmem_st16(pa, p1);
       tmem_st16(pa + 16, p2);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&sm.p_full[g]);
+      // ... and to the other CTA: head h's row of 64 + 64 bytes.
+      if (i >= 1 && !__all_sync(0xffffffffu, mbar_wait_cluster(&sm.pb_free[g ^ 1], (uint32_t)(((i - 1) >> 1) & 1), abort_flag, status, 337))) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        st_async_v4(pb_peer + sw128_offset((uint32_t)h, (uint32_t)c), p1[4 * c], p1[4 * c + 1], p1[4 * c + 2], p1[4 * c + 3], pb_bar);
+        st_async_v4(pb_peer + sw128_offset((uint32_t)h, (uint32_t)c + 4), p2[4 * c], p2[4 * c + 1], p2[4 * c + 2], p2[4 * c + 3], pb_bar);
+      }
+      last_own = i;
     }
-    // Every PV completed.
-    if (ok && J > 0 && (!wait_pv(J - 5) || !wait_pv(J - 2) || !wait_pv(J - 1))) ok = false;
+    // The last tile is the other CTA's: the group whose tile would be next allows its PV.
+    if (ok && J > 0 && (J & 1) == half && ((J >> 1) & 1) == g) ok = wait_pv(J - 4) && take_over(J);
+    // The other CTA is done with this group's P (its commits arrive in this CTA's shared memory).
+    if (ok && last_own >= 0)
+      ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sm.pb_free[g], (uint32_t)((last_own >> 1) & 1), abort_flag, status, 338));
+    // Every PV completed: that of this group's last tile first (of J - 1 - 4 by a wait for J - 1 alone nothing is known).
+    if (ok && J > 0 && ((last_own >= 0 && !wait_pv(2 * last_own + half)) || !wait_pv(J - 1))) ok = false;
     sm.l_g[g][h] = l;
     sm.m_g[g][h] = m_used;
+    {
+      const uint32_t bar = mapa_shared(smem_u32(&sm.ex_full), peer);
+      st_async_b32(mapa_shared(smem_u32(&sm.l_g[2 + g][h]), peer), __float_as_uint(l), bar);
+      st_async_b32(mapa_shared(smem_u32(&sm.m_g[2 + g][h]), peer), __float_as_uint(m_used), bar);
+      if (sw == 0 && lane == 0) mbar_arrive_expect_tx(&sm.ex_full, kPeerSum);
+    }
+    ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sm.ex_full, 0, abort_flag, status, 339)) && ok;
     if (!ok && lane == 0) sm.epi_bad = 1;
     named_bar_sync(1, 2 * kGroup);
     tc_fence_after();
     const bool fin = !sm.epi_bad;
-    // The last published maximum (it only grows) is what O refers to.
-    const float m_fin = fmaxf(sm.m_g[0][h], sm.m_g[1][h]);
+    // The last reference (it only grows) is what O refers to.
+    const float m_fin = fmaxf(fmaxf(sm.m_g[0][h], sm.m_g[1][h]), fmaxf(sm.m_g[2][h], sm.m_g[3][h]));
     float den = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const float li = sm.l_g[i][h];
       if (li != 0.f) den += li * exp2f(sm.m_g[i][h] - m_fin);
     }
@@ -778,11 +888,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
     const bool read_o = J > 0 && any;
     if (fin) {
       const int rope0 = 512 - P.rope_dim;
-      // Rows are staged in shared memory (the stages, then q2's place: every gather and MMA completed), 16 bytes apart
+      // Rows are staged in shared memory (in place of the tiles: every gather and MMA completed), 16 bytes apart
       // against bank conflicts; each warp then sends off the rows of its quadrant, half of them, whole.
       const bool wide = P.splits > 1 || P.out_is_f32;
       const uint32_t row_bytes = wide ? 1024 : 512;
-      uint8_t* srow = stages + (size_t)h * (row_bytes + 16);
+      uint8_t* srow = base + (size_t)h * (row_bytes + 16);
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         const int lc = 128 * g + 32 * cc, col0 = 256 * half + lc;
@@ -822,7 +932,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       const int r0 = 32 * quad + 16 * g, r1 = min(P.H, r0 + 16);
       if (wide) {
         for (int r = r0; r < r1; ++r) {
-          const uint4* src = reinterpret_cast<const uint4*>(stages + (size_t)r * 1040);
+          const uint4* src = reinterpret_cast<const uint4*>(base + (size_t)r * 1040);
           uint4* dst = out + (at + (long long)r * 512) / 4;
           dst[lane] = src[lane];
           dst[32 + lane] = src[32 + lane];
@@ -830,7 +940,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       } else {
 #pragma unroll 4
         for (int r = r0; r < r1; ++r)
-          out[(at + (long long)r * 512) / 8 + lane] = reinterpret_cast<const uint4*>(stages + (size_t)r * 528)[lane];
+          out[(at + (long long)r * 512) / 8 + lane] = reinterpret_cast<const uint4*>(base + (size_t)r * 528)[lane];
       }
     }
   }
@@ -841,6 +951,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
   if (warp == kPvWarp8) tmem_dealloc(tmem, 512);
 }
 
-size_t attn8_smem_bytes() { return 1024 + kStages8 * kStage + kQ2Bytes + sizeof(Smem8); }
+size_t attn8_smem_bytes() { return 1024 + kTileBytes + kQ2Bytes + sizeof(Smem8); }
 
 }  // namespace csa

@@ -181,16 +181,43 @@ __device__ __forceinline__ float split_row(const uint4& a, const uint4& b, RowPi
 // factor each), of a tile's P, a warp's references, the denominators.
 constexpr uint32_t kPeerTile = 2 * 32 * 256, kPeerQ = 64 * (2 * 512 + 4), kPeerP = 128 * 128, kPeerRef = 32 * 8, kPeerSum = 2 * 128 * 8;
 
-// Store lane l's 8 + 8 codes of head `row` into a [4 blocks][128 rows][128 B] swizzled region: of this CTA (at `base`)
-// and of the other (at cluster address `peer`, the bytes counted on its barrier `bar`).
-__device__ __forceinline__ void store_q(uint8_t* base, uint32_t peer, uint32_t bar, int row, int lane, const uint2 (&v)[2]) {
-  const uint32_t off = sw128_offset((uint32_t)row, (uint32_t)((lane & 15) >> 1)) + (uint32_t)(lane & 1) * 8u;
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint2 v) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+
+// Both run once for each row and are not inlined: eight copies each would overrun the instruction cache that the softmax
+// runs from (a window tile took 5 us instead of its 1.3).
+//
+// Split a head's row and store lane l's 8 + 8 codes of each piece at q1 / q2 + off + {0, 2} blocks: of this CTA and of the
+// other (at cluster address + far, the bytes counted on its barrier `bar`). Returns the row's factor.
+__device__ __noinline__ float split_q_row(uint4 a, uint4 c, uint32_t q1, uint32_t q2, uint32_t far1, uint32_t far2, uint32_t bar) {
+  RowPieces pc;
+  const float f = split_row<true>(a, c, pc);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t at = (uint32_t)(2 * i + (lane >> 4)) * kQBlk + off;
-    *reinterpret_cast<uint2*>(base + at) = v[i];
-    st_async_v2(peer + at, v[i].x, v[i].y, bar);
+    const uint32_t at = 2u * i * kQBlk;
+    st_shared_v2(q1 + at, pc.hi[i]);
+    st_async_v2(far1 + at, pc.hi[i].x, pc.hi[i].y, bar);
+    st_shared_v2(q2 + at, pc.lo[i]);
+    st_async_v2(far2 + at, pc.lo[i].x, pc.lo[i].y, bar);
   }
+  return f;
+}
+// Split a window row: its codes of this CTA's 256 dims to `mine`, of the other's to `other` and to the other CTA's
+// slot (cluster address `far`); the second piece kWinRows rows on. Returns the row's scale.
+__device__ __noinline__ float split_window_row(uint4 a, uint4 c, uint32_t mine, uint32_t other, uint32_t far, uint32_t bar, int half) {
+  RowPieces pc;
+  const float s = split_row<false>(a, c, pc);
+#pragma unroll
+  for (int lo = 0; lo < 2; ++lo) {
+    const uint2 v0 = lo ? pc.lo[0] : pc.hi[0], v1 = lo ? pc.lo[1] : pc.hi[1];
+    const uint2 m = half ? v1 : v0, o = half ? v0 : v1;
+    const uint32_t at = lo * kWinRows * 128u;   // (a multiple of 8 rows: the same swizzle)
+    st_shared_v2(mine + at, m);
+    st_shared_v2(other + at, o);
+    st_async_v2(far + at, o.x, o.y, bar);
+  }
+  return s;
 }
 
 // Two 512-dim bf16 rows of a warp, as split_row takes them.
@@ -343,27 +370,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
     };
     // Own window tile w, own tile i: candidate r in rows r and r + 32 of slots A `slot` and B i % 2, and of the other
     // CTA's slot A (its half of the dims).
-    auto window_store = [&](int w, int slot, int i0) {
-      uint8_t* mine = slots_a + (size_t)slot * kSlot;
-      uint8_t* other = slots_b + (size_t)(i0 & 1) * kSlot;
-      const uint32_t far = mapa_shared(smem_u32(mine), peer), bar = mapa_shared(smem_u32(&sm.w_full[slot]), peer);
+    auto window_store = [&](int w, int slot, int own) {
+      const uint32_t mine = smem_u32(slots_a + (size_t)slot * kSlot), other = smem_u32(slots_b + (size_t)(own & 1) * kSlot);
+      const uint32_t far = mapa_shared(mine, peer), bar = mapa_shared(smem_u32(&sm.w_full[slot]), peer);
+      const uint32_t lane_off = (uint32_t)(lane >> 4) * kBlk + (uint32_t)(lane & 1) * 8u;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = 8 * warp + i;
-        RowPieces pc;
-        float s = split_row<false>(wr[i >> 1].a[i & 1], wr[i >> 1].c[i & 1], pc);
-#pragma unroll
-        for (int lo = 0; lo < 2; ++lo) {
-          const uint2 v0 = lo ? pc.lo[0] : pc.hi[0], v1 = lo ? pc.lo[1] : pc.hi[1];
-          const uint2 a = half ? v1 : v0, c = half ? v0 : v1;
-          const uint32_t off = (uint32_t)(lane >> 4) * kBlk + sw128_offset((uint32_t)(r + kWinRows * lo), (uint32_t)((lane & 15) >> 1)) +
-                               (uint32_t)(lane & 1) * 8u;
-          *reinterpret_cast<uint2*>(mine + off) = a;
-          *reinterpret_cast<uint2*>(other + off) = c;
-          st_async_v2(far + off, c.x, c.y, bar);
-        }
+        const uint32_t off = lane_off + sw128_offset((uint32_t)r, (uint32_t)((lane & 15) >> 1));
+        float s = split_window_row(wr[i >> 1].a[i & 1], wr[i >> 1].c[i & 1], mine + off, other + off, far + off, bar, half);
         if (w * kWinRows + r >= nwin) s = 0.f;
-        if (lane < 2) sm.scale[i0 & 3][r + kWinRows * lane] = s;
+        if (lane < 2) sm.scale[own & 3][r + kWinRows * lane] = s;
       }
       fence_proxy_async_smem();
       mbar_arrive(&sm.a_full[slot]);
@@ -424,12 +441,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       if (lk + kRows >= n || J < 2) e1 = -1;
     }
     int next_row = pool_row(e0), next_entry = e1;
-    // The first own window tile is read now, each next one as the one before is stored.
+    // The first own window tile is read behind the first two tiles' gathers (or now, if it is one of them), each next
+    // one as the one before is stored.
+    int first_win = -1;
     {
       bool win = false;
-      int w = 0;
-      for (int j = half; j < J && !win; j += 2) w = tile_of(tile0 + j, Tw, Te, win);
-      if (win) window_read(w);
+      for (int j = half; j < J && !win; j += 2) {
+        first_win = tile_of(tile0 + j, Tw, Te, win);
+        if (win && j < 2) {
+          window_read(first_win);
+          first_win = -1;
+        }
+      }
+      if (!win) first_win = -1;
     }
     int slot = 0;
     uint32_t ph = 0;
@@ -453,11 +477,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
         } else {
           const uint32_t sb = smem_u32(slots_b + (size_t)(i0 & 1) * kSlot);
           const uint32_t st = ((lane >> 4) == half ? sa : sb) + (uint32_t)((lane >> 3) & 1) * kBlk;
+          const uint8_t* src = P.pages + lane * 16;
+          // Rows 8 apart have the same swizzle: two offsets serve all.
+          const uint32_t st0 = st + sw128_offset((uint32_t)warp, (uint32_t)(lane & 7)),
+                         st1 = st + sw128_offset((uint32_t)(warp + 4), (uint32_t)(lane & 7));
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int row = __shfl_sync(0xffffffffu, my_row, i);
-            cp_async_16_zfill(st + sw128_offset((uint32_t)(warp + 4 * i), (uint32_t)(lane & 7)),
-                              P.pages + (long long)max(row, 0) * 512 + lane * 16, row >= 0);
+            cp_async_16_zfill(((i & 1) ? st1 : st0) + (uint32_t)(i >> 1) * 1024u, src + (size_t)(uint32_t)max(row, 0) * 512u, row >= 0);
           }
           if (lane < 16)
             cp_async_4_zfill(smem_u32(&sm.scale[i0 & 3][warp + 4 * lane]), P.scales + (max(my_row, 0) >> P.block_shift),
@@ -468,15 +495,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
         if (pt == 0) mbar_arrive_expect_tx(&sm.w_full[slot], kPeerTile);
         mbar_arrive(&sm.a_full[slot]);
       } else {
-        const uint32_t st = sa + (uint32_t)((lane >> 3) & 1) * kBlk;  // two half rows an instruction
+        // Two half rows an instruction: rows warp + 4 i and warp + 4 (i + 1).
+        const uint32_t st = sa + (uint32_t)((lane >> 3) & 1) * kBlk + sw128_offset((uint32_t)(warp + 4 * (lane >> 4)), (uint32_t)(lane & 7));
+        const uint8_t* src = P.pages + 256 * half + (lane & 15) * 16;
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          const int r = i + (lane >> 4), row = __shfl_sync(0xffffffffu, my_row, r);
-          cp_async_16_zfill(st + sw128_offset((uint32_t)(warp + 4 * r), (uint32_t)(lane & 7)),
-                            P.pages + (long long)max(row, 0) * 512 + 256 * half + (lane & 15) * 16, row >= 0);
+          const int row = __shfl_sync(0xffffffffu, my_row, i + (lane >> 4));
+          cp_async_16_zfill(st + (uint32_t)(i >> 1) * 1024u, src + (size_t)(uint32_t)max(row, 0) * 512u, row >= 0);
         }
         cp_async_arrive_noinc(&sm.a_full[slot]);
       }
+      if (j == 1 && first_win >= 0) window_read(first_win);
       if (++slot == kA) {
         slot = 0;
         ph ^= 1u;
@@ -487,6 +516,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       if (!mbar_wait_cluster(&sm.a_free[j % kA], (uint32_t)((j / kA) & 1), abort_flag, status, 303)) break;
     cp_async_wait_all();  // after an abort: let the copies land before teardown
     if (bad && half == 0) record_status(status, CSA_DEV_BOUNDS);
+    __syncwarp();
+    cluster_arrive_relaxed();
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------ score MMAs of the own tiles
     // The whole warp walks the loop, so that addresses and descriptors stay in uniform registers (a thread by
@@ -538,6 +569,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       mma_commit(&sm.drain[0]);
       mbar_wait_drain(&sm.drain[0], 0, status, 315);
     }
+    __syncwarp();
+    cluster_arrive_relaxed();
   } else if (warp == kPvWarp8) {
     // ------------------------------------------------------------ PV MMAs of every tile
     const bool leader = elect_one();
@@ -598,6 +631,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       mma_commit(&sm.drain[1]);
       mbar_wait_drain(&sm.drain[1], 0, status, 323);
     }
+    __syncwarp();
+    cluster_arrive_relaxed();
   } else {
     // ------------------------------------------------------------ q split, softmax, epilogue
     const int sw = warp - kSoftWarp;           // 0..7
@@ -615,12 +650,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         read_row(w[i >> 1], i & 1, P.q + ((long long)qi * P.H + (row0 + i)) * 512, row0 + i < P.H);
+      const uint32_t lane_off = (uint32_t)(lane >> 4) * kQBlk + (uint32_t)(lane & 1) * 8u;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        RowPieces pc;
-        const float f = split_row<true>(w[i >> 1].a[i & 1], w[i >> 1].c[i & 1], pc) * P.scale_log2;
-        store_q(q1s, q1_peer, bar, row0 + i, lane, pc.hi);
-        store_q(q2, q2_peer, bar, row0 + i, lane, pc.lo);
+        const uint32_t off = lane_off + sw128_offset((uint32_t)(row0 + i), (uint32_t)((lane & 15) >> 1));
+        const float f = split_q_row(w[i >> 1].a[i & 1], w[i >> 1].c[i & 1], smem_u32(q1s) + off, smem_u32(q2) + off, q1_peer + off,
+                                    q2_peer + off, bar) * P.scale_log2;
         if (lane == 0) {
           sm.qf[row0 + i] = f;
           st_async_b32(qf_peer + 4 * (row0 + i), __float_as_uint(f), bar);
@@ -850,6 +885,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
     }
     ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sm.ex_full, 0, abort_flag, status, 339)) && ok;
     if (!ok && lane == 0) sm.epi_bad = 1;
+    __syncwarp();
+    cluster_arrive_relaxed();
     named_bar_sync(1, 2 * kGroup);
     tc_fence_after();
     const bool fin = !sm.epi_bad;
@@ -946,9 +983,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync();  // no access to the other CTA's shared memory after this point
+  __syncthreads();
   tc_fence_after();
   if (warp == kPvWarp8) tmem_dealloc(tmem, 512);
+  // Every role arrived when it was done with the other CTA's shared memory, and saw to it that what the other
+  // CTA sends here had come: relaxed, so that the outputs need not have landed.
+  __syncwarp();
+  cluster_wait();
 }
 
 size_t attn8_smem_bytes() { return 1024 + kTileBytes + kQ2Bytes + sizeof(Smem8); }

@@ -38,7 +38,7 @@ int check_cache(const csa_page_table* pt, const csa_paged_cache* c) {
 }
 
 struct PagesWs {
-  size_t counts, n_moves, list_a, list_b, move_src, move_dst, heir, need, copy, rows, total;
+  size_t n_moves, list_a, list_b, move_src, move_dst, heir, need, copy, rows, total;
 };
 
 PagesWs pages_ws_layout(long long slots, long long max_pages, long long num_pages) {
@@ -49,7 +49,6 @@ PagesWs pages_ws_layout(long long slots, long long max_pages, long long num_page
     off = round_up(off + (size_t)ints * 4, 256);
     return at;
   };
-  w.counts = take(3 * kPagesCluster);
   w.n_moves = take(1);
   w.list_a = take(num_pages);
   w.list_b = take(num_pages);
@@ -74,7 +73,6 @@ int pages_params(const csa_page_table* pt, void* ws, size_t ws_bytes, PagesParam
   P->page_shift = log2_int(pt->page_size);
   P->table = pt->table;
   P->refs = pt->refs;
-  P->counts = reinterpret_cast<int*>(base + w.counts);
   P->n_moves = reinterpret_cast<int*>(base + w.n_moves);
   P->list_a = reinterpret_cast<int*>(base + w.list_a);
   P->list_b = reinterpret_cast<int*>(base + w.list_b);
@@ -188,12 +186,16 @@ int run_attn8(const csa_attn8_args* args, bool list, cudaStream_t st) {
   P.status = reinterpret_cast<uint32_t*>(a.ws);
   const size_t smem = attn8_smem_bytes();
   CSA_CHECK_SUP(smem <= (size_t)dev->max_smem, "shared memory too small for the attention kernel");
-  // Splits: as many as the device's CTA pairs allow per query (and the workspace holds), two tiles of the
-  // longest candidate list a split at least.
+  // Splits: as many as the device's CTA pairs allow per query (and the workspace holds), two tiles of the longest
+  // candidate list a split at least; and only where the tiles that a split saves outweigh the partials and their
+  // merge, which cost as much as 2 tiles and 0.27 a query (of 128 heads). Measured on a B200, one split against all: 24
+  // queries of 12 tiles 28.6 and 29.3 us, of 20 tiles 38.5 and 33.6; 37 queries of 20 tiles 39.4 and 41.9, of 36 tiles 59.8
+  // and 54.1; 8 queries of 8 tiles 23.5 and 20.6; one query of 5 tiles 20.0 and 19.4.
   const long long queries = (long long)a.B * a.S;
   const long long max_tiles = (a.window + 31) / 32 + ((long long)(list ? a.topk : P.max_entries) + 63) / 64;
   int splits = (int)std::min<long long>(attn_ws_splits(queries), std::max<long long>(1, (dev->sms / 2) / queries));
   splits = (int)std::max<long long>(1, std::min<long long>(splits, max_tiles / 2));
+  if (max_tiles * (splits - 1) * 128 * 100 <= splits * (200 * 128 + 27 * queries * a.H)) splits = 1;
   if (splits > 1 && a.ws_bytes < kStatusBytes + attn_part_bytes(queries, splits)) splits = 1;
   P.splits = splits;
   if (splits > 1) {

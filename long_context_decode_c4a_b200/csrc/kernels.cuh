@@ -244,7 +244,7 @@ __global__ void cache_read_kernel(ReadParams P);
 
 constexpr int kPagesCluster = 8;          // CTAs of a page-table operation
 constexpr int kPagesThreads = 1024;
-constexpr int kPagesSmall = 8192;        // places + pages up to which one CTA does the work ...
+constexpr int kPagesSmall = 4096;         // places + pages up to which one CTA does the work ...
 constexpr int kPagesSmallSlots = 2048;    // ... with at most this many slots (their arguments are in shared memory)
 
 struct PagesParams {
@@ -256,7 +256,6 @@ struct PagesParams {
   int32_t* map;                           // compact: [num_pages]
   int32_t* live;                          // compact: [1]
   // workspace
-  int* counts;                            // [3, kPagesCluster]
   int* n_moves;
   int* list_a;                            // [num_pages]
   int* list_b;                            // [num_pages]

@@ -71,27 +71,34 @@ __device__ __forceinline__ void my_run(unsigned n, unsigned& lo, unsigned& hi) {
   hi = min(b, lo + per);
 }
 
-// Scan over all CTAs' threads: the sum of v in the threads before this one, and in all. Ends with a barrier of all, which also
-// orders what was written before it. `slot`: of P.counts, another for each scan.
-template <int C>
-__device__ __forceinline__ int all_scan(int v, int* smem, int* counts, int slot, int& total) {
-  int mine;
-  int r = block_scan(v, smem, mine);
-  if (C == 1) {
-    total = mine;
-    return r;
-  }
-  const int c = (int)rank<C>();
-  if (threadIdx.x == 0) counts[C * slot + c] = mine;
-  all_sync<C>();
-  total = 0;
+// N scans over all CTAs' threads at once: v[k] becomes the sum of v[k] in the threads before this one, total[k] that in
+// all. Ends with a barrier of all, which also orders what was written before it. CTAs exchange their sums through
+// shared memory: `sums` [2][3][kPagesCluster] of each CTA gets every CTA's; `turn`: calls take 0 and 1 in turn, so that a CTA ahead
+// does not overwrite what another still reads.
+template <int C, int N>
+__device__ __forceinline__ void all_scan(int (&v)[N], int (&total)[N], int* smem, int (*sums)[3][kPagesCluster], int turn) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int x = ld_cg(counts + C * slot + i);
-    r += i < c ? x : 0;
-    total += x;
+  for (int k = 0; k < N; ++k) v[k] = block_scan(v[k], smem, total[k]);
+  if (C == 1) return;
+  if (threadIdx.x < C) {
+    const uint32_t far = mapa_shared(smem_u32(&sums[turn][0][rank<C>()]), threadIdx.x);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(far + (uint32_t)(k * kPagesCluster * 4)), "r"(total[k]) : "memory");
   }
-  return r;
+  __syncwarp();
+  all_sync<C>();
+  const int c = (int)rank<C>();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    total[k] = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int x = sums[turn][k][i];
+      v[k] += i < c ? x : 0;
+      total[k] += x;
+    }
+  }
 }
 
 }  // namespace
@@ -288,9 +295,12 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(ReadParams P) 
 //
 // The three table operations are integer scans over the table and the reference counts (64 KB for 64 requests at
 // 32K, a few hundred at a million tokens) in one launch. What they cost is latency: the barriers and dependent loads of
-// each phase, so loads are issued four at a time. Up to kPagesSmall places and pages one CTA is quicker (its
-// barriers cost tens of nanoseconds); beyond, a cluster of 8. What depends on a slot alone is worked out first, by every CTA
-// in its own shared memory (S), or for more than kPagesSmallSlots slots once, in the workspace.
+// each phase, so loads are issued four at a time, and a cluster's CTAs exchange their sums through shared memory (through global
+// memory a reservation took 7.2 us instead of 3.7). Up to kPagesSmall places and pages one CTA is quicker, beyond a
+// cluster of 8; B200, back to back: 4 slots x 8 places, 64 pages: reserve 2.6 (cluster: 3.5), fork 5.2 (7.2), compact
+// 2.8 (4.5) us; 64 x 32, 2048 pages: 3.3 (3.7), 7.0 (8.5), 3.6 (4.9); 64 x 64, 4096 pages: 4.0 (3.7), 8.9 (8.6), 4.9 (4.9); one CTA
+// at 64 x 128, 8192 pages: 6.2, 17.7 and 11.0 against the cluster's 3.9, 9.1 and 5.3. What depends on a slot alone is
+// worked out first, by every CTA in its own shared memory (S), or for more than kPagesSmallSlots slots once, in the workspace.
 
 // f(i, g(i)) for i = first, first + step, ... below n, with four g under way.
 template <typename G, typename F>
@@ -310,8 +320,9 @@ __device__ __forceinline__ void batched(unsigned n, unsigned first, unsigned ste
 // place) order, get the lowest free pages. With fewer free pages than places nothing changes.
 template <int C, bool S>
 __device__ __forceinline__ void pages_reserve(const PagesParams& P) {
-  __shared__ int scan[33];
+  __shared__ int scan[33], sums[2][3][kPagesCluster];
   __shared__ int s_entries[S ? kPagesSmallSlots : 1];
+  if (C > 1) cluster_arrive_relaxed();  // waited for before the first access to another CTA's shared memory
   pdl_wait();
   pdl_trigger();
   const int ps = 1 << P.page_shift, mp = P.max_pages;
@@ -336,15 +347,16 @@ __device__ __forceinline__ void pages_reserve(const PagesParams& P) {
     if (v < 0 && (int)(i - r * mp) < need(r)) ++want;
   });
   batched(f1, f0, 1, [&](unsigned i) { return P.refs[i]; }, [&](unsigned, int v) { nfree += v == 0 ? 1 : 0; });
-  int wall, fall, ball;
-  int w = all_scan<C>(want, scan, P.counts, 0, wall);
-  int f = all_scan<C>(nfree, scan, P.counts, 1, fall);
-  all_scan<C>(bad, scan, P.counts, 2, ball);
+  int at[3] = {want, nfree, bad}, all[3];
+  if (C > 1) cluster_wait();
+  all_scan<C>(at, all, scan, sums, 0);
+  int w = at[0], f = at[1];
+  const int wall = all[0], fall = all[1], ball = all[2];
   if (ball > 0 || wall > fall) {  // the same in every thread
     if (rank<C>() == 0 && threadIdx.x == 0) record_status(P.status, ball > 0 ? CSA_DEV_BOUNDS : CSA_DEV_NO_PAGES);
     return;
   }
-  if (wall == 0) return;
+  if (wall == 0) return;  // (no CTA touches another's shared memory after the scan's barrier)
   for (unsigned i = f0; i < f1 && f < wall; ++i)
     if (P.refs[i] == 0) {
       P.list_a[f++] = (int)i;
@@ -364,9 +376,10 @@ __device__ __forceinline__ void pages_reserve(const PagesParams& P) {
 // free pages are known to suffice: reference counts are worked out in `list_b`, changed rows in `rows`.
 template <int C, bool S>
 __device__ __forceinline__ void pages_fork(const PagesParams& P) {
-  __shared__ int scan[33];
+  __shared__ int scan[33], sums[2][3][kPagesCluster];
   __shared__ int s_parent[S ? kPagesSmallSlots : 1], s_need[S ? kPagesSmallSlots : 1], s_copy[S ? kPagesSmallSlots : 1];
   __shared__ int s_heir[S ? kPagesSmallSlots : 1];
+  if (C > 1) cluster_arrive_relaxed();  // waited for before the first access to another CTA's shared memory
   pdl_wait();
   pdl_trigger();
   const unsigned tid = rank<C>() * kPagesThreads + threadIdx.x;
@@ -393,9 +406,10 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
   });
   batched((unsigned)P.num_pages, tid, kAll, [&](unsigned i) { return P.refs[i]; }, [&](unsigned i, int v) { P.list_b[i] = v; });
   if (tid == 0) *P.n_moves = 0;
-  int ball;
-  all_scan<C>(bad, scan, P.counts, 0, ball);
-  if (ball > 0) {
+  int nbad[1] = {bad}, ball[1];
+  if (C > 1) cluster_wait();
+  all_scan<C>(nbad, ball, scan, sums, 0);
+  if (ball[0] > 0) {
     if (tid == 0) record_status(P.status, CSA_DEV_BOUNDS);
     return;
   }
@@ -437,12 +451,14 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
   my_run<C>((unsigned)P.slots, r0, r1);
   my_run<C>((unsigned)P.num_pages, f0, f1);
   for (unsigned r = r0; r < r1; ++r) want += at(copy, r) >= 0 ? 1 : 0;
-  int wall, fall;
-  int w = all_scan<C>(want, scan, P.counts, 1, wall);
+  all_sync<C>();
   // Phase 3: free pages.
   int nfree = 0;
   batched(f1, f0, 1, [&](unsigned i) { return ld_cg(P.list_b + i); }, [&](unsigned, int v) { nfree += v == 0 ? 1 : 0; });
-  int f = all_scan<C>(nfree, scan, P.counts, 2, fall);
+  int at2[2] = {want, nfree}, all2[2];
+  all_scan<C>(at2, all2, scan, sums, 1);
+  int w = at2[0], f = at2[1];
+  const int wall = all2[0], fall = all2[1];
   if (wall > fall) {
     if (tid == 0) record_status(P.status, CSA_DEV_NO_PAGES);
     return;
@@ -476,19 +492,23 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
 // free page before L. map[p]: where page p is now (-1: it was free).
 template <int C, bool>
 __device__ __forceinline__ void pages_compact(const PagesParams& P) {
-  __shared__ int scan[33];
+  __shared__ int scan[33], sums[2][3][kPagesCluster];
+  if (C > 1) cluster_arrive_relaxed();  // waited for before the first access to another CTA's shared memory
   pdl_wait();
   pdl_trigger();
   const unsigned tid = rank<C>() * kPagesThreads + threadIdx.x;
   constexpr unsigned kAll = C * kPagesThreads;
   unsigned f0, f1;
   my_run<C>((unsigned)P.num_pages, f0, f1);
-  int nlive = 0, L;
+  int nlive = 0;
   batched(f1, f0, 1, [&](unsigned i) { return P.refs[i]; }, [&](unsigned, int v) { nlive += v != 0 ? 1 : 0; });
-  const int before = all_scan<C>(nlive, scan, P.counts, 0, L);  // live pages before f0
+  int at[1] = {nlive}, all[1];
+  if (C > 1) cluster_wait();
+  all_scan<C>(at, all, scan, sums, 0);
+  const int before = at[0], L = all[0];  // live pages before f0, in all
   // Holes (free pages before L), numbered from the front. As many live pages lie at or behind L, and L - 1 - k of
   // them follow page i with k live pages before it, so its number from the front is M - 1 - (L - 1 - k).
-  int holes = 0, M;
+  int holes = 0;
   for (int i = (int)f0, k = before; i < (int)f1; ++i) {
     const bool live = P.refs[i] != 0;
     if (!live && i < L) {
@@ -497,7 +517,9 @@ __device__ __forceinline__ void pages_compact(const PagesParams& P) {
     }
     k += live ? 1 : 0;
   }
-  all_scan<C>(holes, scan, P.counts, 1, M);
+  int at1[1] = {holes}, all1[1];
+  all_scan<C>(at1, all1, scan, sums, 1);
+  const int M = all1[0];
   for (int i = (int)f0, k = before; i < (int)f1; ++i) {
     const bool live = P.refs[i] != 0;
     int to = live ? i : -1;

@@ -75,6 +75,8 @@ int make_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows
 
 }  // namespace
 
+using IndexerKernel = void (*)(CUtensorMap, CUtensorMap, IndexerParams, IndexerFuse);
+
 int device_info(DeviceInfo** out) {
   static DeviceInfo info[64];
   static std::mutex mu;
@@ -95,12 +97,11 @@ int device_info(DeviceInfo** out) {
     CSA_CUDA(cudaFuncSetAttribute(attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
     CSA_CUDA(cudaFuncSetAttribute(attn8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
     CSA_CUDA(cudaFuncSetAttribute(gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
-    CSA_CUDA(cudaFuncSetAttribute(indexer_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
-    CSA_CUDA(cudaFuncSetAttribute(indexer_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
-    CSA_CUDA(cudaFuncSetAttribute(indexer_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
-    CSA_CUDA(cudaFuncSetAttribute(indexer_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
-    CSA_CUDA(cudaFuncSetAttribute(indexer_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
-    CSA_CUDA(cudaFuncSetAttribute(indexer_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
+    for (IndexerKernel k : {indexer_kernel<4, false>, indexer_kernel<8, false>, indexer_kernel<16, false>,
+                            indexer_kernel<32, false>, indexer_kernel<64, false>, indexer_kernel<128, false>,
+                            indexer_kernel<4, true>, indexer_kernel<8, true>, indexer_kernel<16, true>,
+                            indexer_kernel<32, true>, indexer_kernel<64, true>, indexer_kernel<128, true>})
+      CSA_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ms));
     d.attrs_set = true;
   }
   *out = &d;
@@ -331,16 +332,17 @@ int run_indexer_topk(const IndexerArgs& a, cudaStream_t st, cudaEvent_t const* e
       F.flags = reinterpret_cast<uint32_t*>(ws + L.flags_off - shift);
       F.L = *fuse;
     }
-    cudaError_t e = cudaSuccess;
+    const bool paged = a.pt != nullptr;
+    IndexerKernel kernel;
     switch (a.H_I) {
-      case 4: e = launch_pdl(indexer_kernel<4>, grid, dim3(kIdxThreads), smem, st, map_k, map_q, P, F); break;
-      case 8: e = launch_pdl(indexer_kernel<8>, grid, dim3(kIdxThreads), smem, st, map_k, map_q, P, F); break;
-      case 16: e = launch_pdl(indexer_kernel<16>, grid, dim3(kIdxThreads), smem, st, map_k, map_q, P, F); break;
-      case 32: e = launch_pdl(indexer_kernel<32>, grid, dim3(kIdxThreads), smem, st, map_k, map_q, P, F); break;
-      case 64: e = launch_pdl(indexer_kernel<64>, grid, dim3(kIdxThreads), smem, st, map_k, map_q, P, F); break;
-      default: e = launch_pdl(indexer_kernel<128>, grid, dim3(kIdxThreads), smem, st, map_k, map_q, P, F); break;
+      case 4: kernel = paged ? indexer_kernel<4, true> : indexer_kernel<4, false>; break;
+      case 8: kernel = paged ? indexer_kernel<8, true> : indexer_kernel<8, false>; break;
+      case 16: kernel = paged ? indexer_kernel<16, true> : indexer_kernel<16, false>; break;
+      case 32: kernel = paged ? indexer_kernel<32, true> : indexer_kernel<32, false>; break;
+      case 64: kernel = paged ? indexer_kernel<64, true> : indexer_kernel<64, false>; break;
+      default: kernel = paged ? indexer_kernel<128, true> : indexer_kernel<128, false>; break;
     }
-    CSA_CUDA(e);
+    CSA_CUDA(launch_pdl(kernel, grid, dim3(kIdxThreads), smem, st, map_k, map_q, P, F));
   }
   if (ev) CSA_CUDA(cudaEventRecord(ev[0], st));
   if (!run_select) return CSA_OK;

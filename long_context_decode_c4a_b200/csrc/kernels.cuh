@@ -88,7 +88,7 @@ struct IndexerFuse {
   CompressLaunch L;
 };
 
-template <int HI>
+template <int HI, bool kPaged>
 __global__ void indexer_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_q,
                                IndexerParams P, IndexerFuse F);
 

@@ -147,6 +147,7 @@ int run_attn8(const csa_attn8_args* args, bool list, cudaStream_t st) {
   CSA_CHECK_ARG(a.ring_bstride % 8 == 0 && a.ring_bstride >= (int64_t)a.ring_cap * 512,
                 "ring_bstride must be a multiple of 8 and >= ring_cap*512");
   CSA_CHECK_SUP((long long)a.B * a.S * a.H < (1ll << 31), "too many query rows");
+  CSA_CHECK_SUP((long long)a.B * a.S < (1ll << 29), "at most 2^29 queries");
   if (list) {
     CSA_CHECK_ARG(a.topk_idx != nullptr && aligned(a.topk_idx, 4), "topk_idx null or misaligned");
     CSA_CHECK_SUP(a.topk >= 1 && a.topk <= kAttnMaxTopk, "topk must be in [1, %d]", kAttnMaxTopk);

@@ -215,6 +215,14 @@ class Plain:
                 check_close(out, ref, tol, f"{form} split={split}")
 
 
+@pytest.mark.parametrize("W", [1, 33, 97, 128])
+@pytest.mark.parametrize("E", [1, 64, 65, 129, 200, 257, 321, 400, 449, 520, 577, 700, 800])
+def test_every_number_of_tiles(ops, E, W):
+    """1 to 17 tiles, whole and split, odd and even numbers of them on each CTA of a pair, any mix of window and entries."""
+    Plain(ops, E=E, W=W, H=32, t=4 * E + 130, seed=E + W).check(forms=("list",))   # (more are visible than the list has)
+    Plain(ops, E=E, W=W, H=32, t=4 * E + 2, seed=E + W + 1).check(forms=("range",))
+
+
 def test_rising_logits(ops):
     """Scores that climb by far more than the kernel's headroom, tile after tile and row by row."""
     p = Plain(ops)

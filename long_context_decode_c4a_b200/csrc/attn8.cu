@@ -122,13 +122,6 @@ __device__ __forceinline__ uint32_t rest2(uint32_t a, uint32_t b) {
 // Round an fp16 pair to e4m3's 4 significant bits (half a unit away from zero: the code's carry is fp16's).
 __device__ __forceinline__ uint32_t round_e4m3(uint32_t h) { return (h + 0x00400040u) & 0xFF80FF80u; }
 
-// The larger magnitude of two bf16 pairs, the sign undefined; NaN wins.
-__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // Split of a 512-dim bf16 row held by a warp: lane l has dims [8 l, 8 l + 8) in a and [256 + 8 l, ...) in b. The row
 // is scaled to at most 448 in magnitude and taken through fp16, which holds every scaled bf16 value above 2^-14
 // exactly and the rest to 2^-25. Returns 2^k with max |x| <= 448 * 2^k (k >= -100), or NaN if a value is not finite (its

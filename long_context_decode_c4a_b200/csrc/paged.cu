@@ -9,6 +9,7 @@
 
 #include <math_constants.h>
 
+#include "attn_util.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -126,12 +127,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendPara
   const long long u0 = (e0 / P.unit + blockIdx.x) * P.unit;
   if (u0 >= e1 || e1 <= e0) return;
   const long long lp = u0 >> P.page_shift;
-  const int page = lp < P.max_pages ? P.table[(long long)b * P.max_pages + lp] : -1;
-  if (page < 0 || page >= P.num_pages) {
-    if (threadIdx.x == 0) record_status(P.status, CSA_DEV_BOUNDS);
-    return;
-  }
-  const long long row0 = ((long long)page << P.page_shift) + (u0 & ((1 << P.page_shift) - 1));
+  const int page = lp < P.max_pages ? P.table[(long long)b * P.max_pages + lp] : -1;  // looked at behind the rows' reads
   constexpr int kWarps = kAppendThreads / 32, kMax = kAppendMaxUnit / kWarps;
   uint4 a[kMax], c[kMax];
   bool is_new[kMax];
@@ -150,6 +146,11 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendPara
       c[i] = src[32 + lane];
     }
   }
+  if (page < 0 || page >= P.num_pages) {
+    if (threadIdx.x == 0) record_status(P.status, CSA_DEV_BOUNDS);
+    return;
+  }
+  const long long row0 = ((long long)page << P.page_shift) + (u0 & ((1 << P.page_shift) - 1));
 #pragma unroll
   for (int i = 0; i < kMax; ++i) {
     const int r = warp + kWarps * i;
@@ -157,12 +158,10 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendPara
       int k = -1000;                               // no new row
       if (is_new[i]) {
         const uint32_t w[8] = {a[i].x, a[i].y, a[i].z, a[i].w, c[i].x, c[i].y, c[i].z, c[i].w};
-        uint32_t mx = 0;
+        uint32_t mx = w[0];
 #pragma unroll
-        for (int v = 0; v < 8; ++v) mx = __vmaxu2(mx, w[v] & 0x7FFF7FFFu);
-        mx = max(mx & 0xFFFFu, mx >> 16);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int v = 1; v < 8; ++v) mx = max_abs_bf16x2(mx, w[v]);
+        mx = __reduce_max_sync(0xffffffffu, max(mx & 0x7FFFu, (mx >> 16) & 0x7FFFu));
         const int e = (int)(mx >> 7);              // biased exponent; 448 = 1.75 * 2^8
         k = e == 255 ? 1000 : max(-100, e - 127 - 8 + ((mx & 0x7Fu) > 0x60u ? 1 : 0));
       }
@@ -170,17 +169,22 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendPara
     }
   }
   __syncthreads();
-  const int nblk = P.unit >> P.block_shift, block = 1 << P.block_shift;
-  if (threadIdx.x < (unsigned)nblk) {
-    int k = -1000;
-    for (int r = 0; r < block; ++r) k = max(k, row_k[threadIdx.x * block + r]);
-    float* sp = P.scales + (row0 >> P.block_shift) + threadIdx.x;
-    const float old = u0 + (long long)threadIdx.x * block < e0 ? *sp : 0.f;  // a block without earlier rows has none
-    float s = k == 1000 ? CUDART_NAN_F : __uint_as_float((uint32_t)(127 + max(k, -100)) << 23);
-    if (old != old || old > s) s = old;
-    s_old[threadIdx.x] = old;
-    s_new[threadIdx.x] = k == -1000 ? 0.f : s;     // 0: nothing new in the block
-    if (k != -1000) *sp = s;
+  // A thread a row of the unit; the first of each block settles its scale.
+  if (threadIdx.x < (unsigned)P.unit) {  // (16, 32 or 64 of them: whole half warps)
+    const int r = threadIdx.x, block = 1 << P.block_shift;
+    const uint32_t in = P.unit < 32 ? 0xFFFFu : 0xffffffffu;
+    int k = row_k[r];
+    if (block == 64) k = max(k, row_k[r ^ 32]);
+    for (int o = min(block, 32) >> 1; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(in, k, o));
+    if ((r & (block - 1)) == 0) {
+      float* sp = P.scales + ((row0 + r) >> P.block_shift);
+      const float old = u0 + r < e0 ? *sp : 0.f;   // a block without earlier rows has none
+      float s = k == 1000 ? CUDART_NAN_F : __uint_as_float((uint32_t)(127 + max(k, -100)) << 23);
+      if (old != old || old > s) s = old;
+      s_old[r >> P.block_shift] = old;
+      s_new[r >> P.block_shift] = k == -1000 ? 0.f : s;  // 0: nothing new in the block
+      if (k != -1000) *sp = s;
+    }
   }
   __syncthreads();
 #pragma unroll

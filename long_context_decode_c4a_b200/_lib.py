@@ -133,8 +133,8 @@ PROTOTYPES = {
                                  c_void_p]),
     "csa_cache_read": (c_int, [_PT, _PC, c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "csa_pages_reserve": (c_int, [_PT, c_void_p, c_void_p, c_size_t, c_void_p]),
-    "csa_pages_fork": (c_int, [_PT, _PC, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
-    "csa_pages_compact": (c_int, [_PT, _PC, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "csa_pages_fork": (c_int, [_PT, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "csa_pages_compact": (c_int, [_PT, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "csa_indexer_scores_paged": (c_int, [_PT, _PC, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
                                          c_void_p, c_size_t, c_void_p]),
     "csa_indexer_topk_paged": (c_int, [_PT, _PC, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,

@@ -558,6 +558,7 @@ class PagedCache:
             raise ValueError("the cache must be on its page table's device")
         self.book, self.pages, self.scales, self.block, self.d = book, pages, scales, block, pages.shape[2]
         self._arg = PagedCacheArg(self.d, block, pages.data_ptr(), _ptr(scales))
+        self._bytes = bytes(self._arg)
         self._ref, self._addr = ctypes.byref(self._arg), ctypes.addressof(self._arg)
 
     @classmethod
@@ -572,13 +573,12 @@ class PagedCache:
         return cls(book, torch.zeros(book.num_pages, book.page_size, d, dtype=torch.bfloat16, device=book.device))
 
 
-def _cache_list(book: PageTable, caches):
-    arr = (PagedCacheArg * max(1, len(caches)))()
-    for i, c in enumerate(caches):
+def _cache_list(book: PageTable, caches) -> bytes:
+    """The caches' argument structs in a row."""
+    for c in caches:
         if c.book is not book:
             raise ValueError("a cache behind another page table")
-        arr[i] = c._arg
-    return arr
+    return b"".join([c._bytes for c in caches])
 
 
 def cache_append(cache: PagedCache, start_pos: torch.Tensor, S: int, rows: torch.Tensor, ratio: int) -> None:

@@ -342,3 +342,67 @@ def test_indexer_paged_unmapped(ops):
     assert (got[0, 0, 64:128] == 0).all()
     keep = [i for i in range(200) if not 64 <= i < 128]
     assert torch.equal(got[0, 0, keep], full[0, 0, keep])
+
+
+# ------------------------------------------------------------------------------------------------ refusals of the binding
+
+
+def test_bindings_refuse(ops):
+    dev = "cuda"
+    book, other = ops.PageTable.empty(2, 4, 8, 16), ops.PageTable.empty(2, 4, 8, 16)
+    c8, c16 = ops.PagedCache.e4m3(book, 8), ops.PagedCache.bf16(book, 128)
+    z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t, device=dev)  # noqa: E731
+    bf = torch.bfloat16
+    with pytest.raises(TypeError):
+        ops.PageTable(z(2, 4, t=torch.int64), z(8), 16)
+    with pytest.raises(ValueError):
+        ops.PageTable(z(2, 4), z(8), 24)
+    with pytest.raises(ValueError):
+        ops.PageTable(z(8), z(8), 16)
+    for pages, scales in ((z(8, 16, 512, t=bf), z(8, 2, t=torch.float32)), (c8.pages, z(8, 2, t=torch.float64)), (z(8, 16, 128, t=torch.float16), None)):
+        with pytest.raises(TypeError):
+            ops.PagedCache(book, pages, scales)
+    for pages, scales in ((z(7, 16, 128, t=bf), None), (z(8, 32, 128, t=bf), None), (c8.pages, z(8, 3, t=torch.float32)), (c8.pages, z(16, t=torch.float32)),
+                          (c8.pages.cpu(), c8.scales)):
+        with pytest.raises(ValueError):
+            ops.PagedCache(book, pages, scales)
+    rows = z(2, 9, 512, t=bf)
+    for bad in (dict(start_pos=z(2, 1)), dict(rows=z(3, 9, 512, t=bf)), dict(rows=z(2, 9, 128, t=bf)), dict(rows=z(2, 9, 1024, t=bf)[..., ::2]),
+                dict(start_pos=z(2).cpu()), dict(rows=rows.cpu())):
+        with pytest.raises(ValueError):
+            ops.cache_append(c8, **{**dict(start_pos=z(2), S=4, rows=rows, ratio=4), **bad})
+    with pytest.raises(TypeError):
+        ops.cache_append(c8, z(2), 4, rows.float(), 4)
+    with pytest.raises(ops._lib.CsaError):
+        ops.cache_append(c8, z(2), 0, rows, 4)
+    with pytest.raises(ops._lib.CsaError):                     # three requests, two slots
+        ops.cache_read(c8, z(3, 5))
+    for idx, out in ((z(2), None), (z(2, 5), z(2, 5, 128, t=bf))):
+        with pytest.raises(ValueError):
+            ops.cache_read(c8, idx, out=out)
+    with pytest.raises(ValueError):
+        ops.pages_reserve(book, z(3))
+    with pytest.raises(ValueError):
+        ops.pages_fork(book, [ops.PagedCache.bf16(other)], z(2), z(2))
+    with pytest.raises(ValueError):
+        ops.pages_compact(book, [c8], map=z(7))
+    q_idx, w, pos = z(2, 1, 64, 128, t=bf), z(2, 1, 64, t=torch.float32), z(2, 1)
+    for cache in (c8, ops.PagedCache.bf16(book, 64)):
+        with pytest.raises(ValueError):
+            ops.indexer_scores_paged(pos, q_idx, w, cache)
+    with pytest.raises(ValueError):
+        ops.indexer_topk_paged(pos, q_idx, w, c16, 8, scores=z(2, 1, 63, t=torch.float32))
+    q, ring, sink, idx = z(2, 1, 16, 512, t=bf), z(2, 128, 512, t=bf), z(16, t=torch.float32), z(2, 1, 8)
+    for bad in (dict(cache=c16), dict(q=z(2, 1, 16, 256, t=bf)), dict(ring=z(1, 128, 512, t=bf)), dict(sink=z(15, t=torch.float32)), dict(topk_idx=z(2, 8)),
+                dict(out=z(2, 1, 16, 256, t=bf))):
+        with pytest.raises(ValueError):
+            ops.sparse_attn8(**{**dict(q_pos=pos, q=q, ring=ring, cache=c8, topk_idx=idx, sink=sink, window=128), **bad})
+    with pytest.raises(TypeError):
+        ops.hca_attn8(pos, q, ring.float(), c8, sink, 128)
+    with pytest.raises(TypeError):
+        ops.hca_attn8(pos, q, ring, c8, sink, 128, out=z(2, 1, 16, 512, t=torch.float16))
+    for bad in (dict(window=129), dict(window=0), dict(ratio=0), dict(rope_dim=7), dict(scale=float("inf")), dict(ws=z(255, t=torch.uint8))):
+        with pytest.raises(ops._lib.CsaError):
+            ops.hca_attn8(**{**dict(q_pos=pos, q=q, ring=ring, cache=c8, sink=sink, window=128), **bad})
+    assert ops.device_status(book.ws) == 0                      # nothing ran
+    assert (c8.pages.view(torch.uint8) == 0).all() and (book.table == -1).all()

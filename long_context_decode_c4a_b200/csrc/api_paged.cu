@@ -275,7 +275,8 @@ int csa_cache_append(const csa_page_table* pt, const csa_paged_cache* c, int B, 
   if (c->scales != nullptr) {
     P.unit = std::max(c->block, 16);
     const unsigned gx = (unsigned)((n + P.unit - 2) / P.unit + 1);
-    CSA_CUDA(launch_pdl(cache_append_kernel, dim3(gx, (unsigned)B), dim3(kAppendThreads), 0, st, P));
+    void (*kernel)(AppendParams) = P.unit == 16 ? cache_append_kernel<2> : P.unit == 32 ? cache_append_kernel<4> : cache_append_kernel<8>;
+    CSA_CUDA(launch_pdl(kernel, dim3(gx, (unsigned)B), dim3(kAppendThreads), 0, st, P));
   } else {
     const unsigned gx = (unsigned)((n + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
     CSA_CUDA(launch_pdl(cache_append_bf16_kernel, dim3(gx, (unsigned)B), dim3(kAppendThreads), 0, st, P));

@@ -208,7 +208,7 @@ size_t attn8_smem_bytes();
 
 // ------------------------------------------------------------------------------ caches in pages
 
-constexpr int kAppendThreads = 512;
+constexpr int kAppendThreads = 256;
 constexpr int kAppendMaxUnit = 64;        // entries a CTA of the e4m3 append takes: max(block, 16)
 
 struct AppendParams {
@@ -224,6 +224,7 @@ struct AppendParams {
   uint32_t* status;
 };
 
+template <int kMax>
 __global__ void cache_append_kernel(AppendParams P);
 __global__ void cache_append_bf16_kernel(AppendParams P);
 

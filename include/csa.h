@@ -455,9 +455,9 @@ CSA_API int csa_cache_read(const csa_page_table* pt, const csa_paged_cache* cach
  * one, the lowest free pages in (slot, place) order, with refs 1. Places that have a page keep it.
  * csa_pages_fork -- slot r becomes a copy of slot parent[r] (all slots at once; parent[r] == r: unchanged, -1: emptied, its pages
  * freed). entries[s] is the number of entries of slot s that its copies take over. Full pages are shared (refs counts
- * them); of a last page that is partly filled one heir keeps the original (slot s itself if it stays, else its lowest copy)
- * and every other copy gets a page of its own, the lowest free ones in slot order, into which the page is copied in every cache
- * given. So rows appended after a fork never meet another slot's.
+ * them); a last page that is partly filled goes to the lowest of its copies if no other place and no other holder has it after
+ * the call, and every other copy gets a page of its own, the lowest free ones in slot order, into which the page is copied in every
+ * cache given. So the rows appended behind a copy's entries never meet another slot's, nor a page that the caller holds.
  * csa_pages_compact -- the L live pages (refs > 0) become pages 0 .. L-1: the k-th live page at or behind L moves to the
  * k-th free page before L, in every cache given. map[p] = where page p is now, -1 if it was free; *live = L.
  * If a value of the table or the arguments is out of range (CSA_ERR_BOUNDS; compact: the one place is left as it is) or the

@@ -54,7 +54,7 @@ PagesWs pages_ws_layout(long long slots, long long max_pages, long long num_page
   w.list_b = take(num_pages);
   w.move_src = take(num_pages);
   w.move_dst = take(num_pages);
-  w.heir = take(slots);
+  w.heir = take(num_pages);
   w.need = take(slots);
   w.copy = take(slots);
   w.rows = take(slots * max_pages);

@@ -262,7 +262,7 @@ struct PagesParams {
   int* list_b;                            // [num_pages]
   int* move_src;                          // [num_pages]
   int* move_dst;
-  int* heir;                              // [slots]
+  int* heir;                              // [num_pages]
   int* need;                              // [slots]
   int* copy;                              // [slots]
   int* rows;                              // [slots, max_pages]

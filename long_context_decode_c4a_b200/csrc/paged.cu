@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(ReadParams P) 
 // memory a reservation took 7.2 us instead of 3.7). Up to kPagesSmall places and pages one CTA is quicker, beyond a
 // cluster of 8; B200, back to back: 4 slots x 8 places, 64 pages: reserve 2.6 (cluster: 3.5), fork 5.2 (7.2), compact
 // 2.8 (4.5) us; 64 x 32, 2048 pages: 3.3 (3.7), 7.0 (8.5), 3.6 (4.9); 64 x 64, 4096 pages: 4.0 (3.7), 8.9 (8.6), 4.9 (4.9); one CTA
-// at 64 x 128, 8192 pages: 6.2, 17.7 and 11.0 against the cluster's 3.9, 9.1 and 5.3. What depends on a slot alone is
+// at 64 x 128, 8192 pages: 6.2, 17.7 and 11.0 against the cluster's 3.9, 9.3 and 5.3. What depends on a slot alone is
 // worked out first, by every CTA in its own shared memory (S), or for more than kPagesSmallSlots slots once, in the workspace.
 
 // f(i, g(i)) for i = first, first + step, ... below n, with four g under way.
@@ -384,14 +384,15 @@ __device__ __forceinline__ void pages_reserve(const PagesParams& P) {
 }
 
 // Slot r becomes a copy of slot parent[r] (-1: empty, r: unchanged), all slots at once. Pages are shared by
-// reference, except that of several heirs of a partly filled last page one keeps it (the parent's own slot, else
-// the lowest heir) and the others get fresh pages, which pages_copy_kernel fills. Nothing is committed before the
-// free pages are known to suffice: reference counts are worked out in `list_b`, changed rows in `rows`.
+// reference, but for a partly filled last page: rows will be appended to it, so it goes to the lowest of the slots that take
+// it over (`heir`, per page) only if nobody else holds it after the call, and the others get fresh pages, which
+// pages_copy_kernel fills. (The page copied thus always keeps a holder and is never itself a fresh one.) Nothing is
+// committed before the free pages are known to suffice: reference counts, without those of partly filled last pages taken
+// over, are worked out in `list_b`, changed rows in `rows`.
 template <int C, bool S>
 __device__ __forceinline__ void pages_fork(const PagesParams& P) {
   __shared__ int scan[33], sums[2][3][kPagesCluster];
   __shared__ int s_parent[S ? kPagesSmallSlots : 1], s_need[S ? kPagesSmallSlots : 1], s_copy[S ? kPagesSmallSlots : 1];
-  __shared__ int s_heir[S ? kPagesSmallSlots : 1];
   if (C > 1) cluster_arrive_relaxed();  // waited for before the first access to another CTA's shared memory
   pdl_wait();
   pdl_trigger();
@@ -401,23 +402,25 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
   const unsigned cells = (unsigned)P.slots * P.max_pages, mp = P.max_pages;
   // Slots are walked by every CTA where their arrays are its own, by all together otherwise.
   const unsigned s_first = S ? threadIdx.x : tid, s_step = S ? kPagesThreads : kAll;
-  int* heir = S ? s_heir : P.heir;
   int* need = S ? s_need : P.need;    // pages that the slot takes over
-  int* copy = S ? s_copy : P.copy;    // the place of which it takes a copy, -1: none
+  int* copy = S ? s_copy : P.copy;    // the place of its partly filled last page, -1: none; then: if it takes a copy
   auto at = [](int* p, unsigned i) { return S ? p[i] : ld_cg(p + i); };
   auto parent_of = [&](unsigned r) { return S ? s_parent[r] : P.parent[r]; };
+  constexpr int kNone = 0x7FFFFFFF;
   // Phase 0: check, copy the counts, clear the heirs.
   int bad = 0;
   for (unsigned r = s_first; r < (unsigned)P.slots; r += s_step) {
     const int p = P.parent[r], e = P.entries[r];
     if (p < -1 || p >= P.slots || e < 0 || e > cap) bad = 1;
     if (S) s_parent[r] = p;
-    heir[r] = 0x7FFFFFFF;
   }
   batched(cells, tid, kAll, [&](unsigned i) { return P.table[i]; }, [&](unsigned, int v) {
     if (v < -1 || v >= P.num_pages) bad = 1;
   });
-  batched((unsigned)P.num_pages, tid, kAll, [&](unsigned i) { return P.refs[i]; }, [&](unsigned i, int v) { P.list_b[i] = v; });
+  batched((unsigned)P.num_pages, tid, kAll, [&](unsigned i) { return P.refs[i]; }, [&](unsigned i, int v) {
+    P.list_b[i] = v;
+    P.heir[i] = kNone;
+  });
   if (tid == 0) *P.n_moves = 0;
   int nbad[1] = {bad}, ball[1];
   if (C > 1) cluster_wait();
@@ -426,19 +429,18 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
     if (tid == 0) record_status(P.status, CSA_DEV_BOUNDS);
     return;
   }
-  // Phase 1: the lowest heir of each slot that does not keep itself; what each slot takes.
-  for (unsigned r = s_first; r < (unsigned)P.slots; r += s_step) {
-    const int s = parent_of(r);
-    if (s >= 0) atomicMin(heir + s, s == (int)r ? -1 : (int)r);
-  }
-  S ? __syncthreads() : all_sync<C>();
+  // Phase 1: what each slot takes; the lowest heir of each partly filled last page.
   for (unsigned r = s_first; r < (unsigned)P.slots; r += s_step) {
     const int s = parent_of(r);
     int n = 0, c = -1;
     if (s >= 0 && s != (int)r) {
       const int e = P.entries[s];
       n = (int)(((long long)e + ps - 1) >> P.page_shift);
-      if ((e & (ps - 1)) != 0 && at(heir, s) != (int)r && P.table[s * mp + n - 1] >= 0) c = n - 1;
+      const int last = (e & (ps - 1)) != 0 ? P.table[s * mp + n - 1] : -1;
+      if (last >= 0) {
+        c = n - 1;
+        if (!S || r % C == rank<C>()) atomicMin(P.heir + last, (int)r);
+      }
     }
     need[r] = n;
     copy[r] = c;
@@ -463,11 +465,18 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
   unsigned r0, r1, f0, f1;
   my_run<C>((unsigned)P.slots, r0, r1);
   my_run<C>((unsigned)P.num_pages, f0, f1);
-  for (unsigned r = r0; r < r1; ++r) want += at(copy, r) >= 0 ? 1 : 0;
   all_sync<C>();
-  // Phase 3: free pages.
+  for (unsigned r = r0; r < r1; ++r) {  // (these slots' `copy` is this thread's from here on)
+    const int lp = at(copy, r);
+    if (lp < 0) continue;
+    const int p = P.table[(unsigned)parent_of(r) * mp + lp];
+    if (ld_cg(P.list_b + p) == 0 && ld_cg(P.heir + p) == (int)r) copy[r] = -1;
+    else ++want;
+  }
+  // Phase 3: free pages. A page without holders but with an heir stays with that.
   int nfree = 0;
-  batched(f1, f0, 1, [&](unsigned i) { return ld_cg(P.list_b + i); }, [&](unsigned, int v) { nfree += v == 0 ? 1 : 0; });
+  auto count = [&](unsigned i) { return make_int2(ld_cg(P.list_b + i), ld_cg(P.heir + i)); };
+  batched(f1, f0, 1, count, [&](unsigned, int2 v) { nfree += v.x == 0 && v.y == kNone ? 1 : 0; });
   int at2[2] = {want, nfree}, all2[2];
   all_scan<C>(at2, all2, scan, sums, 1);
   int w = at2[0], f = at2[1];
@@ -476,12 +485,14 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
     if (tid == 0) record_status(P.status, CSA_DEV_NO_PAGES);
     return;
   }
-  batched(f1, f0, 1, [&](unsigned i) { return ld_cg(P.list_b + i); }, [&](unsigned i, int v) {
-    if (v == 0 && f < wall) {
+  batched(f1, f0, 1, count, [&](unsigned i, int2 v) {
+    if (v.x == 0 && v.y != kNone) {
+      v.x = 1;
+    } else if (v.x == 0 && f < wall) {
       P.list_a[f++] = (int)i;
-      v = 1;
+      v.x = 1;
     }
-    P.refs[i] = v;
+    P.refs[i] = v.x;
   });
   all_sync<C>();
   // Phase 4: the moves and the changed places (the parents' rows are read before any row changes).

@@ -623,8 +623,8 @@ def pages_reserve(book: PageTable, entries: torch.Tensor) -> None:
 
 def pages_fork(book: PageTable, caches, parent: torch.Tensor, entries: torch.Tensor) -> None:
     """Slot r becomes a copy of the first entries[parent[r]] entries of slot parent[r] (its own number: unchanged,
-    -1: freed), all slots at once: full pages shared, a partly filled last page copied in every cache of `caches`
-    (all behind `book`). parent, entries: int32 [slots]."""
+    -1: freed), all slots at once: full pages shared, a partly filled last page that anybody else has copied in every cache
+    of `caches` (all behind `book`). parent, entries: int32 [slots]."""
     _need(parent, "parent", torch.int32, (book.slots,))
     _need(entries, "entries", torch.int32, (book.slots,))
     _same_device(book._index, parent, entries)

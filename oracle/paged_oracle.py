@@ -6,7 +6,7 @@ TEST INFRASTRUCTURE ONLY; shares no code with the CUDA path.
 from __future__ import annotations
 
 import math
-from typing import Dict, List
+from typing import List
 
 import numpy as np
 
@@ -34,11 +34,7 @@ def reserve(table: List[List[int]], refs: List[int], page: int, entries: List[in
 def fork(table: List[List[int]], refs: List[int], page: int, parent: List[int], entries: List[int]) -> List[tuple]:
     """The pages copied: [(from, to)] in slot order."""
     n = len(parent)
-    kids: Dict[int, List[int]] = {}
-    for r in range(n):
-        if parent[r] >= 0:
-            kids.setdefault(parent[r], []).append(r)
-    new, copies = [], []
+    new, partly, copies = [], [], []
     count = [0] * len(refs)
     for row in table:
         for p in row:
@@ -54,9 +50,8 @@ def fork(table: List[List[int]], refs: List[int], page: int, parent: List[int], 
         if s >= 0:
             need = -(-entries[s] // page)
             row[:need] = table[s][:need]
-            heir = s if parent[s] == s else min(kids[s])
-            if entries[s] % page and heir != r and row[need - 1] >= 0:
-                copies.append((r, need - 1, row[need - 1]))
+            if entries[s] % page and row[need - 1] >= 0:
+                partly.append((r, need - 1, row[need - 1]))
                 row[need - 1] = -2
         new.append(row)
     after = list(outside)
@@ -64,6 +59,12 @@ def fork(table: List[List[int]], refs: List[int], page: int, parent: List[int], 
         for p in row:
             if p >= 0:
                 after[p] += 1
+    for r, lp, p in partly:
+        if after[p] == 0:  # nobody else has it: the lowest slot keeps it
+            new[r][lp] = p
+            after[p] = 1
+        else:
+            copies.append((r, lp, p))
     dst = _take_lowest(after, len(copies))
     for (r, lp, src), p in zip(copies, dst):
         new[r][lp] = p

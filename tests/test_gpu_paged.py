@@ -107,6 +107,42 @@ def test_fork_keep_free(ops, seed, slots, max_pages, page):
     assert ops.device_status(book.ws) == 0
 
 
+@pytest.mark.parametrize("slots", [4, 2500])  # the slots' arguments in shared memory, in the workspace
+@pytest.mark.parametrize("places", [1, 1100])  # one CTA, a cluster
+@pytest.mark.parametrize("table,outside,parent,entries", [
+    ([0, 0, -1, -1], 0, [-1, 1, 0, -1], [9, 16, 0, 0]),     # another slot has all 16 rows
+    ([0, -1, -1, -1], 1, [-1, 0, 0, -1], [9, 0, 0, 0]),     # a holder outside the table
+    ([0, 0, -1, -1], 0, [-1, -1, 1, 0], [9, 7, 0, 0]),      # two parents of one page
+    ([0, 0, -1, -1], 0, [-1, -1, 1, 0], [16, 7, 0, 0]),     # a copy that takes it whole, one that does not
+])
+def test_fork_keeps_no_page_that_another_has(ops, slots, places, table, outside, parent, entries):
+    """Rows appended behind a copy's entries meet nobody else's."""
+    rows = [[p] + [-1] * (places - 1) for p in table] + [[-1] * places for _ in range(slots - 4)]
+    refs = [sum(p == 0 for p in table) + outside] + [0] * 7
+    book = ops.PageTable(i32(rows), i32(refs), 16)
+    cache = ops.PagedCache.bf16(book, 8)
+    cache.pages[0] = torch.arange(16, device="cuda")[:, None].to(torch.bfloat16)
+    pad = [-1] * (slots - 4)
+    moves = PO.fork(rows, refs, 16, parent + pad, entries + [0] * (slots - 4))
+    ops.pages_fork(book, [cache], i32(parent + pad), i32(entries + [0] * (slots - 4)))
+    same_book(book, rows, refs)
+    assert len(moves) == (2 if outside else 1)  # a holder outside: neither heir keeps the page
+    for src, dst in moves:
+        assert src == 0 and torch.equal(cache.pages[dst], cache.pages[0])
+    # Slot r's new rows (its number) behind what it took over.
+    start = [-1 if p < 0 or p == r else entries[p] for r, p in enumerate(parent)]
+    start = [e if 0 <= e < 16 else -1 for e in start]
+    new = torch.arange(4, device="cuda").view(4, 1, 1).expand(4, 16, 8).contiguous().to(torch.bfloat16) + 100
+    ops.cache_append(cache, i32(start), 1, new, 1)
+    assert ops.device_status(book.ws) == 0
+    for r, p in enumerate(parent):
+        if p >= 0:
+            n = entries[p]
+            want = list(range(n)) + ([100 + r] if start[r] >= 0 else [])
+            got = ops.cache_read(cache, i32([list(range(len(want))) if s == r else [-1] * len(want) for s in range(4)]))[r, :, 0]
+            assert got.tolist() == want
+
+
 def test_fork_needs_pages(ops):
     book = ops.PageTable.empty(4, 2, 3, 16)
     ops.pages_reserve(book, i32([20, 0, 0, 0]))

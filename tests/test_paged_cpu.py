@@ -175,6 +175,19 @@ def test_oracle_codes_are_the_format():
         assert PO.block_scale(a) == s
 
 
+def test_oracle_fork_keeps_no_page_that_another_has():
+    """A partly filled last page that somebody else still reads is copied: slot 2 takes 9 of slot 0's 16 entries, slot 1 keeps them all."""
+    tab, refs = [[0], [0], [-1]], [2, 0, 0]
+    assert PO.fork(tab, refs, 16, [-1, 1, 0], [9, 16, 0]) == [(0, 1)]
+    assert tab == [[-1], [0], [1]] and refs == [1, 1, 0]
+    tab, refs = [[0], [-1]], [2, 0]      # ... or a holder outside the table
+    assert PO.fork(tab, refs, 16, [-1, 0], [9, 0]) == [(0, 1)]
+    assert tab == [[-1], [1]] and refs == [1, 1]
+    tab, refs = [[0], [0], [-1], [-1]], [2, 0, 0]   # two parents of one page that both leave: its lowest heir keeps it
+    assert PO.fork(tab, refs, 16, [-1, -1, 1, 0], [9, 7, 0, 0]) == [(0, 1)]
+    assert tab == [[-1], [-1], [0], [1]] and refs == [1, 1, 0]
+
+
 def test_oracle_fork_and_compact_by_hand():
     """Two prompts; slot 1 becomes a sample of slot 0, slot 2 leaves, slot 3 takes slot 2's place in the middle of a page."""
     tab, refs = [[0, 1, -1], [-1, -1, -1], [5, 4, -1], [2, -1, -1]], [1, 1, 1, 0, 1, 1, 0]

@@ -564,6 +564,8 @@ class PagedCache:
     @classmethod
     def e4m3(cls, book: PageTable, block: int = 16) -> "PagedCache":
         """An 8-bit cache of 512-wide entries with a scale for each `block` of them."""
+        if block < 1 or block > min(64, book.page_size) or block & (block - 1):
+            raise ValueError("block must be a power of two in [1, 64], at most page_size")
         return cls(book, torch.zeros(book.num_pages, book.page_size, 512, dtype=torch.float8_e4m3fn, device=book.device),
                    torch.zeros(book.num_pages, book.page_size // block, device=book.device))
 

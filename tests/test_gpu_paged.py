@@ -383,6 +383,13 @@ def test_indexer_paged_unmapped(ops):
 # ------------------------------------------------------------------------------------------------ refusals of the binding
 
 
+@pytest.mark.parametrize("block", [0, -16, 24, 48, 128])
+def test_a_cache_of_another_block_is_refused(ops, block):
+    book = ops.PageTable.empty(2, 2, 4, 64)
+    with pytest.raises(ValueError):
+        ops.PagedCache.e4m3(book, block)
+
+
 def test_bindings_refuse(ops):
     dev = "cuda"
     book, other = ops.PageTable.empty(2, 4, 8, 16), ops.PageTable.empty(2, 4, 8, 16)

@@ -416,7 +416,8 @@ typedef struct {
  *   scales != NULL: 8 bits, d = 512. pages dev uint8 [num_pages, page_size, d] (e4m3 codes); scales dev float
  *     [num_pages, page_size / block], one for each `block` rows (a power of two in [1, 64], at most page_size):
  *     the value of a row is its codes times its block's scale. csa_cache_append writes powers of two, which leave
- *     every value exact in bf16; the attention calls take any positive normal scales (0: the rows do not count).
+ *     every value exact in bf16; the attention calls take any positive normal scales (0: its rows do not count,
+ *     as long as their codes are numbers).
  *   scales == NULL: bf16 rows, pages dev uint16 [num_pages, page_size, d], d a multiple of 8 up to 512, block unused.
  * pages must be 16-byte aligned.
  */

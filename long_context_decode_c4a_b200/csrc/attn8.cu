@@ -48,7 +48,6 @@
 // pipe 24 %, issue slots 28 %): bound by the way of a tile through its stations, gather to PV, that six slots cover, and by
 // 5 us before the first scores (list, q and its split) and 3 after the last PV.
 
-#include <cuda_fp16.h>
 #include <math_constants.h>
 
 #include <cstddef>

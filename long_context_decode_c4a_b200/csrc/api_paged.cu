@@ -190,8 +190,8 @@ int run_attn8(const csa_attn8_args* args, bool list, cudaStream_t st) {
   // Splits: as many as the device's CTA pairs allow per query (and the workspace holds), two tiles of the longest
   // candidate list a split at least; and only where the tiles that a split saves outweigh the partials and their
   // merge, which cost as much as 2 tiles and 0.27 a query (of 128 heads). Measured on a B200, one split against all: 24
-  // queries of 12 tiles 28.6 and 29.3 us, of 20 tiles 38.5 and 33.6; 37 queries of 20 tiles 39.4 and 41.9, of 36 tiles 59.8
-  // and 54.1; 8 queries of 8 tiles 23.5 and 20.6; one query of 5 tiles 20.0 and 19.4.
+  // queries of 12 tiles 27.8 and 28.9 us, of 20 tiles 37.1 and 32.6; 37 queries of 20 tiles 38.5 and 40.3, of 36 tiles 58.1
+  // and 52.5; 8 queries of 8 tiles 22.2 and 20.7, of 5 tiles 19.2 and 21.2; one query of 8 tiles 22.0 and 18.1.
   const long long queries = (long long)a.B * a.S;
   const long long max_tiles = (a.window + 31) / 32 + ((long long)(list ? a.topk : P.max_entries) + 63) / 64;
   int splits = (int)std::min<long long>(attn_ws_splits(queries), std::max<long long>(1, (dev->sms / 2) / queries));

@@ -36,15 +36,15 @@
 //     256 dims (own tiles, until their scores are there), a buffer for the other CTA's P; q2 (64 KB).
 //   Warps: 0..3 split window rows and gather entries (16-byte cp.async); 4 issues the score MMAs, 5 the PV MMAs
 //     (and owns TMEM); 6..9 and 10..13 are the softmax groups of even and odd own tiles, one head (TMEM lane)
-//     a thread; both first split q (each CTA half of the heads, for both), and share the epilogue.
+//     a thread; both first split q (each CTA half of the heads, for both) and own tile 1's window rows, and share the epilogue.
 //   The reference of P and O (the maximum, when it last had to be raised) is handed from tile to tile, so across the
 //     CTAs each time: the group of tile j takes over that of tile j - 1, rescales its CTA's O if it changed, allows
 //     PV(j - 1) (ack), raises it if its own scores ask for it, and hands it on before it forms P.
 // Split-candidate mode (few queries): as in attn.cu; attn_combine_kernel merges the partials.
 //
-// One B200, in a graph: 64 requests at 32K (1024 of 8192 entries and 128 window rows each) 43.6 us, 0.27 of the time that the
-// operations need at the dense bf16 rate and 0.21 of the HBM copy rate; a segment of 2000 queries 1142 us (0.32 of the
-// former); 24 requests of 1500 entries 37.9 us; one request of 39 entries 19.7 us. No unit is near its limit (tensor
+// One B200, in a graph: 64 requests at 32K (1024 of 8192 entries and 128 window rows each) 42.2 us, 0.28 of the time that the
+// operations need at the dense bf16 rate and 0.21 of the HBM copy rate; a segment of 2000 queries 1092 us (0.33 of the
+// former); 24 requests of 1500 entries 36.4 us; one request of 39 entries 19.4 us. No unit is near its limit (tensor
 // pipe 24 %, issue slots 28 %): bound by the way of a tile through its stations, gather to PV, that six slots cover, and by
 // 5 us before the first scores (list, q and its split) and 3 after the last PV.
 
@@ -240,22 +240,32 @@ __device__ __forceinline__ void split_p(float p0, float p1, float p2, float p3, 
   c2 = codes_e5m2(rest2(h0, a0) + 0x00800080u, rest2(h1, a1) + 0x00800080u);
 }
 
-// Order of a query's tiles: two entry tiles first, whose gathers are quick, then pairs of window and of entry tiles in turn while
-// both last, the rest of the window, the rest of the entries: the split of a window tile takes the gathering warps longer than
-// the tensor cores need for a tile. (Pairs, so that each CTA owns half of the window; and it spreads the window
-// over the splits of a query.) Returns the index of tile p among those of its kind.
+// Order of a query's tiles. Three window tiles or more (the usual window of 128 has four): four of them first, which the
+// gathering and the softmax warps split while there is nothing else to do. Then, or with fewer from the start, two entry
+// tiles, then pairs of window and of entry tiles in turn while both last, the rest of the window, the rest of the
+// entries: further on the split of a window tile takes the gathering warps longer than the tensor cores need for a tile. (Pairs,
+// so that each CTA owns half of the window.) B200, 64 queries of 1024 entries, window first and entries first: 16 rows 39.9 and
+// 38.0 us, 64 rows 40.2 and 39.0, 80 rows 40.9 and 42.2, 128 rows 42.2 and 44.0, 512 rows 73.5 and 75.7.
+__device__ __forceinline__ int first_window(int Tw) { return Tw >= 3 ? min(Tw, 4) : 0; }
+// The index of tile p among those of its kind.
 __device__ __forceinline__ int tile_of(int p, int Tw, int Te, bool& win) {
-  const int alt = Te < 2 ? 0 : min(Tw >> 1, (Te - 2) >> 1), e0 = Te < 2 ? 0 : 2, q = p - e0;
-  win = false;
+  const int first = first_window(Tw), rest = Tw - first;
+  win = p < first;
+  if (win) return p;
+  p -= first;
+  if (rest == 0) return p;
+  const int alt = Te < 2 ? 0 : min(rest >> 1, (Te - 2) >> 1), e0 = Te < 2 ? 0 : 2, q = p - e0;
   if (q < 0) return p;
   if (q < 4 * alt) {
     win = (q & 2) == 0;
-    return (q >> 2) * 2 + (q & 1) + (win ? 0 : e0);
+    return (q >> 2) * 2 + (q & 1) + (win ? first : e0);
   }
-  const int r = q - 4 * alt, w = 2 * alt + r;  // the first of what is left is window tile 2 alt
-  win = w < Tw;
-  return win ? w : e0 + 2 * alt + (w - Tw);
+  const int w = 2 * alt + q - 4 * alt;  // the first of what is left is the (2 alt)-th of the rest
+  win = w < rest;
+  return win ? first + w : e0 + 2 * alt + (w - rest);
 }
+// No window tile lies at this position or behind it.
+__device__ __forceinline__ int window_end(int Tw) { return Tw == first_window(Tw) ? Tw : 2 * Tw + 2 - first_window(Tw); }
 
 // Two fp32 operations an instruction.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -348,49 +358,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
   const int ecap = t < 0 ? 0 : min((int)(((long long)t + 1) / P.ratio), P.max_entries);
   // Tile j (of this item's J) is CTA j % 2's own, the (j >> 1)-th of them; it lies in slot A j % kA.
 
+  // N candidates of window tile w, from the r0-th on, into a warp's registers ...
+  auto window_read = [&](auto& rows, int w, int r0) {
+    constexpr int N = 2 * sizeof(rows) / sizeof(RowPair);
+    const uint16_t* ring = P.ring + (long long)b * P.ring_bstride;
+    const int k0 = w * kWinRows + r0;
+    int slot = (p0 + (k0 < nwin ? k0 : 0)) % P.ring_cap;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      read_row(rows[i >> 1], i & 1, ring + (long long)slot * 512, k0 + i < nwin);
+      slot = slot + 1 == P.ring_cap ? 0 : slot + 1;
+    }
+  };
+  // ... and their pieces into slots A `slot` and B own % 2 of own tile `own`, and the other CTA's slot A (its half of the
+  // dims): candidate r in rows r and r + 32.
+  auto window_store = [&](auto& rows, int w, int r0, int slot, int own) {
+    constexpr int N = 2 * sizeof(rows) / sizeof(RowPair);
+    const uint32_t mine = smem_u32(slots_a + (size_t)slot * kSlot), other = smem_u32(slots_b + (size_t)(own & 1) * kSlot);
+    const uint32_t far = mapa_shared(mine, peer), bar = mapa_shared(smem_u32(&sm.w_full[slot]), peer);
+    const uint32_t lane_off = (uint32_t)(lane >> 4) * kBlk + (uint32_t)(lane & 1) * 8u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = r0 + i;
+      const uint32_t off = lane_off + sw128_offset((uint32_t)r, (uint32_t)((lane & 15) >> 1));
+      float s = split_window_row(rows[i >> 1].a[i & 1], rows[i >> 1].c[i & 1], mine + off, other + off, far + off, bar, half);
+      if (w * kWinRows + r >= nwin) s = 0.f;
+      if (lane < 2) sm.scale[own & 3][r + kWinRows * lane] = s;
+    }
+    fence_proxy_async_smem();
+  };
+
   if (warp < kProd / 32) {
     // ------------------------------------------------------------ window split, gathers
     const int pt = threadIdx.x;
     const int32_t* table = P.table + (long long)b * P.max_pages;
-    const uint16_t* ring = P.ring + (long long)b * P.ring_bstride;
     const int32_t* sel = P.topk_idx == nullptr ? nullptr : P.topk_idx + (long long)qi * P.topk;
     bool bad = false;
-    // This warp's candidates of window tile w: rows 8 warp .. + 7, read an own window tile ahead.
-    RowPair wr[4];
-    auto window_read = [&](int w) {
-      const int k0 = w * kWinRows + 8 * warp;
-      int slot = (p0 + (k0 < nwin ? k0 : 0)) % P.ring_cap;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        read_row(wr[i >> 1], i & 1, ring + (long long)slot * 512, k0 + i < nwin);
-        slot = slot + 1 == P.ring_cap ? 0 : slot + 1;
-      }
-    };
-    // Own window tile w, own tile i: candidate r in rows r and r + 32 of slots A `slot` and B i % 2, and of the other
-    // CTA's slot A (its half of the dims).
-    auto window_store = [&](int w, int slot, int own) {
-      const uint32_t mine = smem_u32(slots_a + (size_t)slot * kSlot), other = smem_u32(slots_b + (size_t)(own & 1) * kSlot);
-      const uint32_t far = mapa_shared(mine, peer), bar = mapa_shared(smem_u32(&sm.w_full[slot]), peer);
-      const uint32_t lane_off = (uint32_t)(lane >> 4) * kBlk + (uint32_t)(lane & 1) * 8u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 8 * warp + i;
-        const uint32_t off = lane_off + sw128_offset((uint32_t)r, (uint32_t)((lane & 15) >> 1));
-        float s = split_window_row(wr[i >> 1].a[i & 1], wr[i >> 1].c[i & 1], mine + off, other + off, far + off, bar, half);
-        if (w * kWinRows + r >= nwin) s = 0.f;
-        if (lane < 2) sm.scale[own & 3][r + kWinRows * lane] = s;
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&sm.a_full[slot]);
-    };
-
     // Number of candidates: up to the last valid place of the list (-1 in between is a masked row), or every entry.
-    // The entries of the first two tiles are read with the list, before the count is known.
     const int lk = warp + 4 * (lane & 15);  // the row of a tile that lane i < 16 looks after
-    int n = ecap, e0 = lk, e1 = lk + kRows;
+    // The gathering warps split own tile 0, if it is of the window (8 rows a warp), and own tiles from 2 on; the softmax warps
+    // own tile 1.
+    RowPair wr[4];
+    const bool early = P.splits == 1 && half < first_window(Tw);
+    if (early) window_read(wr, half, 8 * warp);  // in flight while the list is looked through
+    int n = ecap, s0 = lk, s1 = lk + kRows;
     if (sel != nullptr) {
-      e0 = lk < P.topk ? sel[lk] : -1;
-      e1 = lk + kRows < P.topk ? sel[lk + kRows] : -1;
+      s0 = lk < P.topk ? sel[lk] : -1;
+      s1 = lk + kRows < P.topk ? sel[lk + kRows] : -1;
       int last = 0;
       for (int j = pt; j < P.topk; j += kProd)
         if (sel[j] >= 0) last = j + 1;
@@ -431,28 +445,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       }
       return (pg << P.page_shift) | (e & ((1 << P.page_shift) - 1));
     };
-    if (tile0 > 0 || Te < 2) {  // (with two entry tiles or more, a query's first two tiles are these)
-      e0 = entry_of(0);
-      e1 = entry_of(1);
-    } else {
-      if (lk >= n || J < 1) e0 = -1;
-      if (lk + kRows >= n || J < 2) e1 = -1;
-    }
-    int next_row = pool_row(e0), next_entry = e1;
-    // The first own window tile is read behind the first two tiles' gathers (or now, if it is one of them), each next
-    // one as the one before is stored.
-    int first_win = -1;
-    {
-      bool win = false;
-      for (int j = half; j < J && !win; j += 2) {
-        first_win = tile_of(tile0 + j, Tw, Te, win);
-        if (win && j < 2) {
-          window_read(first_win);
-          first_win = -1;
+    auto begin = [&](int j) -> int {
+      bool win;
+      const int i = tile_of(tile0 + j, Tw, Te, win), k = i * kRows + lk;
+      if (j >= J || win || k >= n) return -1;
+      return i == 0 ? s0 : i == 1 ? s1 : sel != nullptr ? sel[k] : k;
+    };
+    int next_row = pool_row(begin(0)), next_entry = begin(1);
+    // The next own window tile behind tile j that these warps split, into registers.
+    auto next_window = [&](int j) {
+      for (j += 2; j < J && tile0 + j < window_end(Tw); j += 2) {
+        bool win;
+        const int w = tile_of(tile0 + j, Tw, Te, win);
+        if (win && j >> 1 != 1) {
+          window_read(wr, w, 8 * warp);
+          return;
         }
       }
-      if (!win) first_win = -1;
-    }
+    };
+    if (!early) next_window(half - 2);
     int slot = 0;
     uint32_t ph = 0;
     for (int j = 0; j < J; ++j) {
@@ -470,8 +481,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       if ((j & 1) == half) {
         if (i0 >= 2 && !mbar_wait(&sm.b_free[i0 & 1], (uint32_t)((i0 >> 1) & 1) ^ 1u, abort_flag, status, 304)) break;
         if (win) {
-          window_store(index, slot, i0);
-          if (index + 2 < Tw) window_read(index + 2);
+          if (i0 != 1) {
+            window_store(wr, index, 8 * warp, slot, i0);
+            mbar_arrive(&sm.a_full[slot]);
+            next_window(j);
+          }
         } else {
           const uint32_t sb = smem_u32(slots_b + (size_t)(i0 & 1) * kSlot);
           const uint32_t st = ((lane >> 4) == half ? sa : sb) + (uint32_t)((lane >> 3) & 1) * kBlk;
@@ -503,7 +517,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
         }
         cp_async_arrive_noinc(&sm.a_full[slot]);
       }
-      if (j == 1 && first_win >= 0) window_read(first_win);
       if (++slot == kA) {
         slot = 0;
         ph ^= 1u;
@@ -682,6 +695,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
     mbar_arrive(&sm.q_done);
     mbar_arrive_remote_relaxed(mapa_shared(smem_u32(&sm.q_done), peer));  // this thread has read its part of the staging area
 
+    // Own tile 1, if it is of the window: four rows a warp.
+    ok = __all_sync(0xffffffffu, mbar_wait(&sm.list_ready, 0, abort_flag, status, 331)) && ok;
+    {
+      bool win = false;
+      const int j = half + 2, w = ok && j < sm.n_tiles ? tile_of(sm.tile0 + j, Tw, sm.entry_tiles, win) : 0;
+      if (win) {
+        RowPair rows[2];
+        window_read(rows, w, 4 * sw);
+        // (Slot A 3 is in the staging area, here and in the other CTA.)
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sm.q_done, 0, abort_flag, status, 340)) && ok;
+        if (ok) window_store(rows, w, 4 * sw, j, 1);
+        __syncwarp();
+        if (ok && lane < 16) mbar_arrive(&sm.a_full[j]);  // eight warps: kProd arrivals
+      }
+    }
+
     // Inverse-RoPE table for position t, while the first scores are on their way (the epilogue's barrier orders it).
     const int st = threadIdx.x - kSoftWarp * 32;  // 0..255
     if (st < P.rope_dim / 2) {
@@ -690,7 +719,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       sm.rope_cs[st][0] = cs;
       sm.rope_cs[st][1] = -sn;
     }
-    ok = __all_sync(0xffffffffu, mbar_wait(&sm.list_ready, 0, abort_flag, status, 331)) && ok;
     const int J = ok ? sm.n_tiles : 0;
     const int tile0 = sm.tile0, Te = sm.entry_tiles;
     const float qf = sm.qf[h];

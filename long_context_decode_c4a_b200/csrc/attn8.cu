@@ -466,20 +466,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
     if (!early) next_window(half - 2);
     int slot = 0;
     uint32_t ph = 0;
+    // A lane whose wait ran out stays in the loop (its later waits return at once, and the output is given up): the warp's
+    // shuffles need all lanes, and a vote on each wait costs 2.5 % of the kernel.
     for (int j = 0; j < J; ++j) {
       const int my_row = next_row;
       next_row = pool_row(next_entry);
       next_entry = entry_of(j + 2);
-      if (j >= kA) {
-        if (!mbar_wait_cluster(&sm.a_free[slot], ph ^ 1u, abort_flag, status, 302)) break;
-      } else if (j >= 3) {
-        if (!mbar_wait_cluster(&sm.q_done, 0, abort_flag, status, 301)) break;
-      }
+      if (j >= kA) mbar_wait_cluster(&sm.a_free[slot], ph ^ 1u, abort_flag, status, 302);
+      else if (j >= 3) mbar_wait_cluster(&sm.q_done, 0, abort_flag, status, 301);
       bool win;
       const int index = tile_of(tile0 + j, Tw, Te, win), i0 = j >> 1;
       const uint32_t sa = smem_u32(slots_a + (size_t)slot * kSlot);
       if ((j & 1) == half) {
-        if (i0 >= 2 && !mbar_wait(&sm.b_free[i0 & 1], (uint32_t)((i0 >> 1) & 1) ^ 1u, abort_flag, status, 304)) break;
+        if (i0 >= 2) mbar_wait(&sm.b_free[i0 & 1], (uint32_t)((i0 >> 1) & 1) ^ 1u, abort_flag, status, 304);
         if (win) {
           if (i0 != 1) {
             window_store(wr, index, 8 * warp, slot, i0);

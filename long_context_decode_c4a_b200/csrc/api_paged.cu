@@ -38,7 +38,7 @@ int check_cache(const csa_page_table* pt, const csa_paged_cache* c) {
 }
 
 struct PagesWs {
-  size_t n_moves, list_a, list_b, move_src, move_dst, heir, need, copy, rows, total;
+  size_t n_moves, list_a, list_b, move_src, move_dst, heir, need, copy, last, rows, total;
 };
 
 PagesWs pages_ws_layout(long long slots, long long max_pages, long long num_pages) {
@@ -57,6 +57,7 @@ PagesWs pages_ws_layout(long long slots, long long max_pages, long long num_page
   w.heir = take(num_pages);
   w.need = take(slots);
   w.copy = take(slots);
+  w.last = take(slots);
   w.rows = take(slots * max_pages);
   w.total = off;
   return w;
@@ -81,6 +82,7 @@ int pages_params(const csa_page_table* pt, void* ws, size_t ws_bytes, PagesParam
   P->heir = reinterpret_cast<int*>(base + w.heir);
   P->need = reinterpret_cast<int*>(base + w.need);
   P->copy = reinterpret_cast<int*>(base + w.copy);
+  P->last = reinterpret_cast<int*>(base + w.last);
   P->rows = reinterpret_cast<int*>(base + w.rows);
   P->status = reinterpret_cast<uint32_t*>(ws);
   return CSA_OK;

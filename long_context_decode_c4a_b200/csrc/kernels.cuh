@@ -265,6 +265,7 @@ struct PagesParams {
   int* heir;                              // [num_pages]
   int* need;                              // [slots]
   int* copy;                              // [slots]
+  int* last;                              // [slots]
   int* rows;                              // [slots, max_pages]
   uint32_t* status;
 };

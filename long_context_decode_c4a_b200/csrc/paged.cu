@@ -310,9 +310,9 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(ReadParams P) 
 // 32K, a few hundred at a million tokens) in one launch. What they cost is latency: the barriers and dependent loads of
 // each phase, so loads are issued four at a time, and a cluster's CTAs exchange their sums through shared memory (through global
 // memory a reservation took 7.2 us instead of 3.7). Up to kPagesSmall places and pages one CTA is quicker, beyond a
-// cluster of 8; B200, back to back: 4 slots x 8 places, 64 pages: reserve 2.6 (cluster: 3.5), fork 5.2 (7.2), compact
-// 2.8 (4.5) us; 64 x 32, 2048 pages: 3.3 (3.7), 7.0 (8.5), 3.6 (4.9); 64 x 64, 4096 pages: 4.0 (3.7), 8.9 (8.6), 4.9 (4.9); one CTA
-// at 64 x 128, 8192 pages: 6.2, 17.7 and 11.0 against the cluster's 3.9, 9.3 and 5.3. What depends on a slot alone is
+// cluster of 8; B200, back to back: 4 slots x 8 places, 64 pages: reserve 2.6 (cluster: 3.5), fork 5.0 (7.2), compact
+// 2.8 (4.5) us; 64 x 32, 2048 pages: 3.3 (3.7), 6.9 (8.5), 3.8 (4.9); 64 x 64, 4096 pages: 4.0 (3.7), 8.9 (9.0), 4.9 (5.1); one CTA
+// at 64 x 128, 8192 pages: 6.2, 17.7 and 11.0 against the cluster's 3.9, 9.4 and 5.3. What depends on a slot alone is
 // worked out first, by every CTA in its own shared memory (S), or for more than kPagesSmallSlots slots once, in the workspace.
 
 // f(i, g(i)) for i = first, first + step, ... below n, with four g under way.
@@ -393,6 +393,7 @@ template <int C, bool S>
 __device__ __forceinline__ void pages_fork(const PagesParams& P) {
   __shared__ int scan[33], sums[2][3][kPagesCluster];
   __shared__ int s_parent[S ? kPagesSmallSlots : 1], s_need[S ? kPagesSmallSlots : 1], s_copy[S ? kPagesSmallSlots : 1];
+  __shared__ int s_last[S ? kPagesSmallSlots : 1];
   if (C > 1) cluster_arrive_relaxed();  // waited for before the first access to another CTA's shared memory
   pdl_wait();
   pdl_trigger();
@@ -404,6 +405,7 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
   const unsigned s_first = S ? threadIdx.x : tid, s_step = S ? kPagesThreads : kAll;
   int* need = S ? s_need : P.need;    // pages that the slot takes over
   int* copy = S ? s_copy : P.copy;    // the place of its partly filled last page, -1: none; then: if it takes a copy
+  int* last = S ? s_last : P.last;    // that page
   auto at = [](int* p, unsigned i) { return S ? p[i] : ld_cg(p + i); };
   auto parent_of = [&](unsigned r) { return S ? s_parent[r] : P.parent[r]; };
   constexpr int kNone = 0x7FFFFFFF;
@@ -432,18 +434,19 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
   // Phase 1: what each slot takes; the lowest heir of each partly filled last page.
   for (unsigned r = s_first; r < (unsigned)P.slots; r += s_step) {
     const int s = parent_of(r);
-    int n = 0, c = -1;
+    int n = 0, c = -1, p = -1;
     if (s >= 0 && s != (int)r) {
       const int e = P.entries[s];
       n = (int)(((long long)e + ps - 1) >> P.page_shift);
-      const int last = (e & (ps - 1)) != 0 ? P.table[s * mp + n - 1] : -1;
-      if (last >= 0) {
+      p = (e & (ps - 1)) != 0 ? P.table[s * mp + n - 1] : -1;
+      if (p >= 0) {
         c = n - 1;
-        if (!S || r % C == rank<C>()) atomicMin(P.heir + last, (int)r);
+        if (!S || r % C == rank<C>()) atomicMin(P.heir + p, (int)r);
       }
     }
     need[r] = n;
     copy[r] = c;
+    last[r] = p;
   }
   S ? __syncthreads() : all_sync<C>();
   // Phase 2: changed rows and counts.
@@ -467,9 +470,8 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
   my_run<C>((unsigned)P.num_pages, f0, f1);
   all_sync<C>();
   for (unsigned r = r0; r < r1; ++r) {  // (these slots' `copy` is this thread's from here on)
-    const int lp = at(copy, r);
-    if (lp < 0) continue;
-    const int p = P.table[(unsigned)parent_of(r) * mp + lp];
+    const int p = at(last, r);
+    if (p < 0) continue;
     if (ld_cg(P.list_b + p) == 0 && ld_cg(P.heir + p) == (int)r) copy[r] = -1;
     else ++want;
   }
@@ -500,7 +502,7 @@ __device__ __forceinline__ void pages_fork(const PagesParams& P) {
     const int lp = at(copy, r);
     if (lp < 0) continue;
     const int dst = ld_cg(P.list_a + w);
-    P.move_src[w] = P.table[(unsigned)parent_of(r) * mp + lp];
+    P.move_src[w] = at(last, r);
     P.move_dst[w] = dst;
     ++w;
     P.rows[r * mp + lp] = dst;

@@ -45,7 +45,7 @@
 // One B200, in a graph: 64 requests at 32K (1024 of 8192 entries and 128 window rows each) 42.2 us, 0.28 of the time that the
 // operations need at the dense bf16 rate and 0.21 of the HBM copy rate; a segment of 2000 queries 1092 us (0.33 of the
 // former); 24 requests of 1500 entries 36.4 us; one request of 39 entries 19.4 us. No unit is near its limit (tensor
-// pipe 24 %, issue slots 28 %): bound by the way of a tile through its stations, gather to PV, that six slots cover, and by
+// pipe 23 %, issue slots 27 %): bound by the way of a tile through its stations, gather to PV, that six slots cover, and by
 // 5 us before the first scores (list, q and its split) and 3 after the last PV.
 
 #include <math_constants.h>

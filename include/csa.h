@@ -496,7 +496,7 @@ typedef struct {
   const uint16_t* q;             /* dev bf16 [B, S, H, 512] */
   const uint16_t* ring;          /* dev bf16, slot j of request b at ring + b*ring_bstride + j*512 */
   const int32_t* topk_idx;       /* dev [B, S, topk], -1: none (hca_attn8: not looked at) */
-  const float* sink;             /* dev [H] */
+  const float* sink;             /* dev [H]; -inf: none, +inf: it has all of the weight (the head's output is zero) */
   void* out;                     /* dev [B, S, H, 512]: bf16, or float if out_is_f32 */
   void* ws;
   size_t ws_bytes;

@@ -746,7 +746,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         if (done) {
           const float lb = sm.l_b[h], mb = sm.m_b[h];
           const float mf = fmaxf(m_used, mb);  // the last published max (it only grows): O's reference
-          l = (l != 0.f ? l * exp2f(m_used - mf) : 0.f) + (lb != 0.f ? lb * exp2f(mb - mf) : 0.f);
+          // (No difference of two that are +inf, as a sink may be: the sink then has all of the weight.)
+          l = (l == 0.f || m_used == mf ? l : l * exp2f(m_used - mf)) + (lb == 0.f || mb == mf ? lb : lb * exp2f(mb - mf));
           m_fin = mf;
         }
         sm.inv_l[h] = 1.f / l;
@@ -844,7 +845,8 @@ __global__ void __launch_bounds__(kAttnCombineThreads) attn_combine_kernel(AttnC
     for (int u = 0; u < 4; ++u) {
       const int s = s0 + u;
       if (s < ns) {
-        const float w = ms[s] == -CUDART_INF_F ? 0.f : exp2f(ms[s] - M);
+        // (The larger reference has weight 1 even where it is +inf, a sink's.)
+        const float w = ms[s] == -CUDART_INF_F ? 0.f : ms[s] == M ? 1.f : exp2f(ms[s] - M);
         L += w * ls[s];
         acc.x += w * o[u].x;
         acc.y += w * o[u].y;

@@ -932,12 +932,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       f = any ? (1.f / 256.f) / den : 0.f;
     } else {
       // A partial refers to its own maximum; split 0's denominator holds the sink, and refers to the
-      // sink if that is larger.
+      // sink if that is larger (+inf too: the sink then has all of the weight). A padding query has neither.
       f = 1.f / 256.f;
-      if (sp == 0 && sl > -CUDART_INF_F) {
+      if (sp == 0 && t >= 0 && sl != -CUDART_INF_F) {
         const float r = fmaxf(ref, sl);
         const float w = any ? exp2f(ref - r) : 0.f;
-        den = (den != 0.f ? den * w : 0.f) + exp2f(sl - r);
+        den = (den != 0.f ? den * w : 0.f) + (sl == r ? 1.f : exp2f(sl - r));
         f *= w;
         ref = r;
       }

@@ -515,6 +515,10 @@ typedef struct {
  *   segment's queries are all there if ring_cap >= window + S - 1 (the caller's choice, not checked).
  *   Pointers 16-byte aligned. ws: csa_workspace_size(CSA_WS_SPARSE_ATTN, ...) / CSA_WS_HCA_ATTN, or only its
  *   status word (slower for few queries).
+ * Precision: the softmax weights of the numerator are held in two 8-bit pieces. A weight (times its block's scale) is off by at
+ * most 2^-8 of itself down to 2^-9 of the row's largest, by more below: 2^-3 of itself at 2^-14. One below 2^-20 of the largest adds
+ * nothing for up to 26 tiles of 64 candidates; for longer lists that limit falls with the number of tiles, to 2^-25 from 854 on, so that a
+ * long tail is not lost. The denominator is the sum of the whole weights. q, window rows: see csrc/attn8.cu.
  * A selected entry that is not visible at t, a visible one (range form) beyond the table, or an entry whose page is
  * not mapped is skipped and records CSA_ERR_BOUNDS.
  */

@@ -16,10 +16,11 @@
 //     a tile); exact down to 2^-10 of the row's largest element, off by at most 2^-17 of it below. Its score is the
 //     sum of the two columns, its P stands in both.
 //   P = p1 + p2: p1 is P rounded to e4m3 (4 significant bits), p2 the remainder rounded to e5m2 (3 bits), so
-//     P is off by at most 2^-8 of itself (p1 leaves 2^-4, p2 leaves 2^-4 of that: a step below a bf16 P's
-//     2^-9). Where p1 is subnormal (P below 2^-14, a weight below 2^-9 of the row's largest), it is off by at most
-//     2^-22 and 2^-4 of itself (2^-17 of the largest weight); a long flat tail behind one large weight is
-//     still there: e5m2 reaches 2^-24, 7 bits below e4m3.
+//     P is off by at most 2^-8 of itself (p1 leaves 2^-4 of its binade, p2 2^-4 of that). A bf16 P's worst case is the same,
+//     its mean square 2.8 times as large; the P_hi + P_lo of attn.cu (2^-16) would take a third and a fourth piece
+//     here, and the tensor memory that holds P is full with two. P below 2^-14, where p1 is subnormal, is off by at most
+//     2^-22; below 2^-18 p2 alone has it, by at most 2^-3 of itself (and fp16's 2^-25); below 2^-25 nothing is left.
+//     (In units where the largest P lies between 2^-4.25 and 2^0.75; kHeadMost says what that means for a long tail.)
 // P carries the scale of its column (O += (p_j s_j) c_j), so the running maximum is that of
 // y_j = l_j + log2 s_j; the denominator takes P back to p_j with 1 / s_j. The sink enters at the end
 // only: it must not push P below e4m3's range.
@@ -75,9 +76,14 @@ constexpr uint32_t kQBlk = 128 * 128;           // one 128-dim block of a q piec
 constexpr uint32_t kQ2Bytes = 4 * kQBlk;        // 64 KB
 // TMEM columns.
 constexpr uint32_t kScoreCol = 128, kPCol = 192, kOCol = 256;
-// P is formed relative to 2^(m + kHead), m the running maximum when O was last rescaled: later rows may exceed m
-// by 2^(kHead + kOver) before O has to be rescaled again, P staying at or below 1.75 (e4m3's 448).
-constexpr float kHead = 4.25f, kOver = 0.75f;
+// P is formed relative to 2^ref, the reference ref = m + head, m the running maximum when O was last rescaled: later rows may
+// exceed ref by 2^kOver before O has to be rescaled again, P staying at or below 1.75 (e4m3's 448). Headroom costs the weights
+// far below the largest: P below 2^-14 is off by up to 2^-22, its pieces' steps there, which J tiles can add up to
+// 64 J 2^(head - 22) of the largest weight. So head is what keeps that below 2^-7 (P's own precision is 2^-8): kHeadMost up to 26
+// tiles, then a binade less for each doubling, and none from 854 tiles on (54592 candidates a pair), beyond which the bound grows with
+// the number of tiles. Less for few tiles would cost: 64 queries of 20 tiles took 42.6 us at 4.25, 44.4 at 3.7, as one of a
+// warp's 32 heads needs a rescale more often; on long lists new maxima are rare.
+constexpr float kHeadMost = 4.25f, kHeadLeast = -0.75f, kOver = 0.75f;
 static_assert(kAttn8Threads == 32 * (kSoftWarp + 8), "warp roles");
 
 struct Smem8 {
@@ -101,6 +107,7 @@ struct Smem8 {
   uint32_t tmem_base;
   int abort_flag, epi_bad;
   int n_tiles, tile0, entry_tiles;
+  float head;              // how far the reference is set above the maximum
   int last[kProd / 32];
   float rope_cs[kMaxRopePairs][2];
   float qf[128];           // per head: 2^k_h * scale * log2(e)
@@ -422,6 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       sm.n_tiles = J;
       sm.tile0 = tile0;
       sm.entry_tiles = Te;
+      sm.head = fminf(kHeadMost, fmaxf(kHeadLeast, 9.f - log2f((float)max(J, 1))));
       mbar_arrive(&sm.list_ready);
     }
 
@@ -728,10 +736,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
     auto wait_pv = [&](int i) -> bool {
       return i < 0 || __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[i & 3], (uint32_t)((i / 4) & 1), abort_flag, status, 332));
     };
-    float m_used = -CUDART_INF_F, l = 0.f;
-    // O from reference m0 to m (in the lanes where that is larger).
-    auto rescale = [&](float m0, float m) {
-      const float alpha = m > m0 ? exp2f(m0 - m) : 1.f;
+    float ref = -CUDART_INF_F, l = 0.f;
+    // O from reference r0 to r (in the lanes where that is larger).
+    auto rescale = [&](float r0, float r) {
+      const float alpha = r > r0 ? exp2f(r0 - r) : 1.f;
       const uint64_t alpha2 = pack2(alpha, alpha);
       tc_fence_after();
 #pragma unroll 1
@@ -752,11 +760,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       tmem_wait_st();
       tc_fence_before();
     };
-    // This group's sum from reference m_used to m.
-    auto refer_to = [&](float m) {
-      if (m > m_used) {
-        l = l != 0.f ? l * exp2f(m_used - m) : 0.f;
-        m_used = m;
+    // This group's sum from reference ref to r.
+    auto refer_to = [&](float r) {
+      if (r > ref) {
+        l = l != 0.f ? l * exp2f(ref - r) : 0.f;
+        ref = r;
       }
     };
     // Take over the reference after tile j - 1, the other CTA's, and allow its PV here.
@@ -841,19 +849,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       if (j == 0) mbar_arrive(&sm.ack[g]);  // (keeps the barrier's phases in step)
       // Raise the reference where the scores ask for it; the TMEM accesses are warp-collective, so the warp takes
       // the branch if any lane must.
-      const float m_before = m_used;
-      const bool need = mt > m_used + (kHead + kOver) || (m_used == -CUDART_INF_F && mt > m_used);
+      const float ref_before = ref;
+      const bool need = mt > ref + kOver || (ref == -CUDART_INF_F && mt > ref);
       if (__any_sync(0xffffffffu, need)) {
         if (!wait_pv(j - 1)) {
           ok = false;
           break;
         }
-        if (j > 0) rescale(m_before, need ? mt : m_before);
-        if (need) refer_to(mt);
+        const float to = mt + sm.head;  // (the same in both CTAs)
+        if (j > 0) rescale(ref_before, need ? to : ref_before);
+        if (need) refer_to(to);
       }
-      st_async_v2(hand_peer, __float_as_uint(m_before), __float_as_uint(m_used), hand_bar);
-      const float ref = (m_used == -CUDART_INF_F ? 0.f : m_used) + kHead;
-      const uint64_t ref2 = pack2(-ref, -ref);
+      st_async_v2(hand_peer, __float_as_uint(ref_before), __float_as_uint(ref), hand_bar);
+      const float minus = ref == -CUDART_INF_F ? 0.f : -ref;
+      const uint64_t ref2 = pack2(minus, minus);
       uint32_t p1[16], p2[16];
       uint64_t ls[2] = {0, 0};
 #pragma unroll
@@ -901,11 +910,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
     // Every PV completed: that of this group's last tile first (of J - 1 - 4 by a wait for J - 1 alone nothing is known).
     if (ok && J > 0 && ((last_own >= 0 && !wait_pv(2 * last_own + half)) || !wait_pv(J - 1))) ok = false;
     sm.l_g[g][h] = l;
-    sm.m_g[g][h] = m_used;
+    sm.m_g[g][h] = ref;
     {
       const uint32_t bar = mapa_shared(smem_u32(&sm.ex_full), peer);
       st_async_b32(mapa_shared(smem_u32(&sm.l_g[2 + g][h]), peer), __float_as_uint(l), bar);
-      st_async_b32(mapa_shared(smem_u32(&sm.m_g[2 + g][h]), peer), __float_as_uint(m_used), bar);
+      st_async_b32(mapa_shared(smem_u32(&sm.m_g[2 + g][h]), peer), __float_as_uint(ref), bar);
       if (sw == 0 && lane == 0) mbar_arrive_expect_tx(&sm.ex_full, kPeerSum);
     }
     ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sm.ex_full, 0, abort_flag, status, 339)) && ok;
@@ -916,15 +925,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
     tc_fence_after();
     const bool fin = !sm.epi_bad;
     // The last reference (it only grows) is what O refers to.
-    const float m_fin = fmaxf(fmaxf(sm.m_g[0][h], sm.m_g[1][h]), fmaxf(sm.m_g[2][h], sm.m_g[3][h]));
+    const float fin_ref = fmaxf(fmaxf(sm.m_g[0][h], sm.m_g[1][h]), fmaxf(sm.m_g[2][h], sm.m_g[3][h]));
     float den = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float li = sm.l_g[i][h];
-      if (li != 0.f) den += li * exp2f(sm.m_g[i][h] - m_fin);
+      if (li != 0.f) den += li * exp2f(sm.m_g[i][h] - fin_ref);
     }
-    const bool any = m_fin != -CUDART_INF_F || den != den;  // some candidate counted (or the row is NaN)
-    float ref = m_fin + kHead;
+    const bool any = fin_ref != -CUDART_INF_F || den != den;  // some candidate counted (or the row is NaN)
+    ref = fin_ref;
     const float sl = h < P.H ? P.sink[h] * 1.4426950408889634f : -CUDART_INF_F;
     float f;                                   // what O is multiplied by
     if (P.splits == 1) {
@@ -934,10 +943,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttn8Threads, 1) at
       // A partial refers to its own maximum; split 0's denominator holds the sink, and refers to the
       // sink if that is larger (+inf too: the sink then has all of the weight). A padding query has neither.
       f = 1.f / 256.f;
-      if (sp == 0 && t >= 0 && sl != -CUDART_INF_F) {
+      if (sp == 0 && Tw > 0 && sl != -CUDART_INF_F) {
         const float r = fmaxf(ref, sl);
         const float w = any ? exp2f(ref - r) : 0.f;
-        den = (den != 0.f ? den * w : 0.f) + (sl == r ? 1.f : exp2f(sl - r));
+        den = (den != 0.f ? den * w : 0.f) + exp2f(sl == r ? 0.f : sl - r);
         f *= w;
         ref = r;
       }

@@ -82,3 +82,46 @@ def test_infinite_sink_in_the_contiguous_form(ops, split):
     assert (outs[1][5] == 0).all()
     rest = [h for h in range(H) if h != 5]
     assert torch.equal(outs[0][rest], outs[1][rest])
+
+
+# ------------------------------------------------------------------------------------------------ long tails
+
+
+@pytest.mark.parametrize("W", [1, 128])
+@pytest.mark.parametrize("f", [1.1875, 1.265625, 1.28125, 1.34375])
+def test_long_tail_behind_one_large_weight(ops, f, W):
+    """262144 visible entries of weights around 2^-19.4 to 2^-21.9 of the largest, most of a quarter of its mass: they count.
+    All but one page hold the same 64 rows, so the sums are taken over those."""
+    g = torch.Generator().manual_seed(int(64 * f))
+    places, page = 4096, 64
+    book = ops.PageTable(i32([[0] + [1] * (places - 1)]), i32([1, places - 1]), page)
+    u = torch.ones(D)
+    u[1::2] = -1
+    rows = (torch.randint(0, 2, (2, page, D // 2), generator=g) * 2.0 - 1).repeat_interleave(2, -1)   # no part along u
+    rows[1, :, :16] += (torch.randint(-1, 2, (page, 1), generator=g) * 0.25 * u[:16])                 # or a little: l within 0.18
+    rows[0, 7] = u * 0.5                                                                               # the large one
+    cache = ops.PagedCache(book, rows.to(torch.float8_e4m3fn).cuda(), torch.ones(2, page // 16, device="cuda"))
+    rows = rows.to(torch.float8_e4m3fn).double().numpy()
+    H = 8
+    q = (u * f).to(torch.bfloat16).expand(1, 1, H, D).contiguous()
+    ring, sink = torch.zeros(1, W, D, dtype=torch.bfloat16), torch.full((H,), -INF)
+    out = torch.empty(1, 1, H, D, dtype=torch.float32, device="cuda")
+    ws = ops.workspace(ops._lib.CSA_WS_HCA_ATTN, 1, 1, 1, 1)
+    c = np.concatenate([np.zeros((1, D)), rows.reshape(-1, D)])
+    n = np.array([W] + [1] * page + [places - 1] * page, dtype=np.float64)
+    l = np64(q[0, 0, 0]) @ c.T / math.sqrt(D)
+    w = np.exp(l - l.max())
+    ref = O.rope(((n * w) @ c / (n * w).sum())[None], 4 * places * page - 1, 64, 10000.0, inverse=True)[0]
+    # A weight's P is w 2^-head, head what the reference is above the maximum: -0.75 for the 4097 tiles or more of one pair, 1 for a
+    # sixteenth of them. Below 2^-18 its second piece alone has it: three bits, 2^-3 of itself at most, and 2^-25 for fp16's
+    # step below 2^-14. Else it is off by 2^-8 of itself, or 2^-22 and 2^-4 of itself. The denominator has it whole. Scores and
+    # additions: 2^-13.
+    for head, part in ((-0.75, ws[:256]), (1.0, ws)):
+        P = w * 2.0 ** -head
+        dP = np.where(P < 2.0 ** -18, P * 2.0 ** -3 + 2.0 ** -25, np.minimum(2.0 ** -8 * P + 2.0 ** -22, 2.0 ** -4 * P))
+        tol = (n * (dP * 2.0 ** head + 2.0 ** -13 * w)) @ np.abs(c) / (n * w).sum()
+        tol[D - 64:] = tol[D - 64:].reshape(-1, 2).sum(-1).repeat(2)
+        ops.hca_attn8(i32([[4 * places * page - 1]]), q.cuda(), ring.cuda(), cache, sink.cuda(), W, ratio=4, out=out, ws=part)
+        assert ops.device_status(ws) == 0
+        for h in range(H):
+            check_close(out[0, 0, h], ref, tol, f"head={head}")

@@ -461,8 +461,9 @@ CSA_API int csa_cache_read(const csa_page_table* pt, const csa_paged_cache* cach
  * cache given. So the rows appended behind a copy's entries never meet another slot's, nor a page that the caller holds.
  * csa_pages_compact -- the L live pages (refs > 0) become pages 0 .. L-1: the k-th live page at or behind L moves to the
  * k-th free page before L, in every cache given. map[p] = where page p is now, -1 if it was free; *live = L.
- * If a value of the table or the arguments is out of range (CSA_ERR_BOUNDS; compact: the one place is left as it is) or the
- * free pages do not suffice (CSA_ERR_NO_PAGES), the code is recorded in the status word and reserve and fork change nothing.
+ * If a value of the table or the arguments is out of range, or an entry that a copy takes over has no page (CSA_ERR_BOUNDS; compact:
+ * the one place is left as it is), or the free pages do not suffice (CSA_ERR_NO_PAGES), the code is recorded in the status word and
+ * reserve and fork change nothing.
  *   entries, parent dev int32 [slots]; map dev int32 [num_pages]; live dev int32 [1].
  *   caches: host array of n_caches; every cache behind the table whose rows are to follow (0 .. 1024).
  *   ws/ws_bytes: workspace of at least csa_workspace_size(CSA_WS_PAGES, slots, max_pages, num_pages, 0). Its contents do not

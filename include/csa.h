@@ -434,8 +434,9 @@ typedef struct {
  * request to skip. 8-bit caches: a block's scale becomes the least power of two 2^k (k >= -100) with max |x| <= 448 * 2^k over its
  * rows, and never less than it was while the block has earlier rows (rows of entries below start_pos/ratio), whose codes are
  * rounded again if it grows. Each value is rounded to the nearest code. A row with a value that is not finite makes its
- * block's scale NaN (and the block's later readers NaN). Pages of the entries must be mapped and not shared with
- * another slot; an entry whose page is not mapped, or whose g >= max_rows, is left out and records CSA_ERR_BOUNDS.
+ * block's scale NaN (and the block's later readers NaN). An entry whose page is not mapped or shared with another slot (refs above 1,
+ * and another slot has the page at the same place, as after csa_pages_fork), or whose g >= max_rows, is left out and records
+ * CSA_ERR_BOUNDS. A page that only the caller holds besides is written: rows behind the entries that it is held for are the slot's.
  *   start_pos dev int32 [B]; rows dev bf16, 16-byte aligned, rows_bstride a multiple of 8.
  *   ws: at least 256 bytes (status word), as in csa_cache_read.
  */

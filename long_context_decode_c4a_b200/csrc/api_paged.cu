@@ -266,6 +266,8 @@ int csa_cache_append(const csa_page_table* pt, const csa_paged_cache* c, int B, 
   P.pages = static_cast<uint8_t*>(c->pages);
   P.scales = c->scales;
   P.table = pt->table;
+  P.refs = pt->refs;
+  P.slots = pt->slots;
   P.num_pages = pt->num_pages;
   P.page_shift = log2_int(pt->page_size);
   P.block_shift = c->scales ? log2_int(c->block) : 0;

@@ -220,7 +220,8 @@ struct AppendParams {
   uint8_t* pages;
   float* scales;
   const int32_t* table;
-  int num_pages, page_shift, block_shift, max_pages, unit;
+  const int32_t* refs;                    // [num_pages]: holders of each page
+  int slots, num_pages, page_shift, block_shift, max_pages, unit;
   uint32_t* status;
 };
 

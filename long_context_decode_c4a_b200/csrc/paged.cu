@@ -106,12 +106,20 @@ __device__ __forceinline__ void all_scan(int (&v)[N], int (&total)[N], int* smem
 
 // ------------------------------------------------------------------------------------------------ append
 
+// Whether a slot other than b has `page` at place lp too (a fork gives copies their pages at the parent's places). The threads
+// of a warp or a CTA, `first` of `step`, look at their part of the slots; looked at only where the page has several holders.
+__device__ __forceinline__ bool others_page(const AppendParams& P, int b, long long lp, int page, int first, int step) {
+  bool other = false;
+  for (int s = first; s < P.slots; s += step) other |= s != b && P.table[(long long)s * P.max_pages + lp] == page;
+  return other;
+}
+
 // Entries [e0, e1) that a segment of S tokens at start_pos completes, from `rows` into the pages (e4m3).
 // A CTA takes one unit of max(block, 16) entries (a block's rows share its scale, and a unit lies inside
 // one page); a warp takes a row at a time, 16 dims a lane, and keeps it in registers between the block's maximum
-// and the rounding, so every row is read once. Bound by latency: the position, then rows and page, the scale, the
-// codes. B200: one entry of 64 requests 2.7 us, 8192 entries (8.4 MB read, 4.2 written) 4.6 (6.5 with 16 warps a CTA, whose
-// registers leave two CTAs an SM).
+// and the rounding, so every row is read once. Bound by latency: the position, then rows and page, then the page's holders and the
+// block's scale, the codes. B200: one entry of 64 requests 2.5 us, 8192 entries (8.4 MB read, 4.2 written) 4.3 (with 16 warps a
+// CTA, whose registers leave two CTAs an SM, 2 us more).
 //   scale of a block = the least power of two 2^k with max |x| <= 448 * 2^k over its rows, and never less
 //   than before: when new rows raise it, the earlier rows' codes are rounded again to the new step (by an exact
 //   power of two; only codes below e4m3's normal range lose bits).
@@ -155,6 +163,11 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendPara
     return;
   }
   const long long row0 = ((long long)page << P.page_shift) + (u0 & ((1 << P.page_shift) - 1));
+  // The page's holders, and the scale so far of the block that the thread's row begins: on their way beside the rows.
+  const int held = P.refs[page], r0 = threadIdx.x, block = 1 << P.block_shift;
+  float* sp = P.scales + ((row0 + r0) >> P.block_shift);
+  const bool begins = r0 < P.unit && (r0 & (block - 1)) == 0;
+  const float old = begins && u0 + r0 < e0 ? *sp : 0.f;  // (a block without earlier rows has none)
 #pragma unroll
   for (int i = 0; i < kMax; ++i) {
     const int r = warp + kWarps * i;
@@ -172,17 +185,20 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendPara
       if (lane == 0) row_k[r] = k;
     }
   }
+  // Rows are not written over another slot's.
+  if (held > 1 && __syncthreads_or(others_page(P, b, lp, page, threadIdx.x, kAppendThreads))) {
+    if (threadIdx.x == 0) record_status(P.status, CSA_DEV_BOUNDS);
+    return;
+  }
   __syncthreads();
   // A thread a row of the unit; the first of each block settles its scale.
   if (threadIdx.x < (unsigned)P.unit) {  // (16, 32 or 64 of them: whole half warps)
-    const int r = threadIdx.x, block = 1 << P.block_shift;
+    const int r = r0;
     const uint32_t in = P.unit < 32 ? 0xFFFFu : 0xffffffffu;
     int k = row_k[r];
     if (block == 64) k = max(k, row_k[r ^ 32]);
     for (int o = min(block, 32) >> 1; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(in, k, o));
-    if ((r & (block - 1)) == 0) {
-      float* sp = P.scales + ((row0 + r) >> P.block_shift);
-      const float old = u0 + r < e0 ? *sp : 0.f;   // a block without earlier rows has none
+    if (begins) {
       float s = k == 1000 ? CUDART_NAN_F : __uint_as_float((uint32_t)(127 + max(k, -100)) << 23);
       if (old != old || old > s) s = old;
       s_old[r >> P.block_shift] = old;
@@ -258,7 +274,18 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_bf16_kernel(Appen
   const long long row = ((long long)page << P.page_shift) + (e & ((1 << P.page_shift) - 1));
   const uint4* src = reinterpret_cast<const uint4*>(P.rows + (long long)b * P.rows_bstride + e * P.d);
   uint4* dst = reinterpret_cast<uint4*>(P.pages + row * P.d * 2);
-  for (int i = lane; i < P.d / 8; i += 32) dst[i] = src[i];
+  const int held = P.refs[page];
+  uint4 v[2];  // d is at most 512
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 32 * i < P.d / 8) v[i] = src[lane + 32 * i];
+  if (held > 1 && __any_sync(0xffffffffu, others_page(P, b, lp, page, lane, 32))) {
+    if (lane == 0) record_status(P.status, CSA_DEV_BOUNDS);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 32 * i < P.d / 8) dst[lane + 32 * i] = v[i];
 }
 
 // ------------------------------------------------------------------------------------------------ read

@@ -586,7 +586,8 @@ def _cache_list(book: PageTable, caches) -> bytes:
 def cache_append(cache: PagedCache, start_pos: torch.Tensor, S: int, rows: torch.Tensor, ratio: int) -> None:
     """Write the entries that a segment of S tokens at start_pos [B] completes from rows [B, max_rows, d] bf16 (entry
     g in row g, where compress() leaves it) into the cache's pages; start_pos < 0 skips a request. Quantises
-    into an 8-bit cache, whose blocks' scales grow as needed. The status word is in cache.book.ws."""
+    into an 8-bit cache, whose blocks' scales grow as needed. Entries without a page of the slot's own (none, or one that another
+    slot shares) are left out and reported. The status word is in cache.book.ws."""
     book = cache.book
     _need(start_pos, "start_pos", torch.int32)
     B = start_pos.shape[0]

@@ -503,7 +503,22 @@ def _same_device(device: int, *tensors) -> None:
         raise ValueError(f"the tensors are on cuda:{device}: make it the current device (torch.cuda.device) for the call")
 
 
-class PageTable:
+class _Handle:
+    """Holds tensors whose addresses its C struct has: what __init__ set (up to `_fixed`) stays, so that no other tensor takes the
+    place of one that the kernels go on reading and writing."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__.get("_fixed", ()):
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed: make another {type(self).__name__} for other tensors")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        if name in self.__dict__.get("_fixed", ()):
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed")
+        super().__delattr__(name)
+
+
+class PageTable(_Handle):
     """Pages of the caches behind it: slot r (request r of a call) holds entry e in row e % page_size of page
     table[r, e // page_size] (-1: no page). refs[p] counts the holders of page p, 0: free. Both live on the GPU and change in
     stream order; a workspace for the page-table calls (with the device status word of every call behind the
@@ -527,6 +542,7 @@ class PageTable:
         self._ws = self.ws.data_ptr(), self.ws.numel()
         self._arg = PageTableArg(self.slots, self.max_pages, self.num_pages, page_size, table.data_ptr(), refs.data_ptr())
         self._ref, self._addr = ctypes.byref(self._arg), ctypes.addressof(self._arg)
+        self._fixed = frozenset(self.__dict__)
 
     @classmethod
     def empty(cls, slots: int, max_pages: int, num_pages: int, page_size: int = 64, device="cuda") -> "PageTable":
@@ -535,7 +551,7 @@ class PageTable:
                    torch.zeros(num_pages, dtype=torch.int32, device=device), page_size)
 
 
-class PagedCache:
+class PagedCache(_Handle):
     """A cache behind a page table: pages [num_pages, page_size, 512] of e4m3 codes with scales [num_pages,
     page_size // block] (fp32, one per block of rows), or pages [num_pages, page_size, d] of bf16 rows without scales."""
 
@@ -560,6 +576,7 @@ class PagedCache:
         self._arg = PagedCacheArg(self.d, block, pages.data_ptr(), _ptr(scales))
         self._bytes = bytes(self._arg)
         self._ref, self._addr = ctypes.byref(self._arg), ctypes.addressof(self._arg)
+        self._fixed = frozenset(self.__dict__)
 
     @classmethod
     def e4m3(cls, book: PageTable, block: int = 16) -> "PagedCache":

@@ -85,3 +85,20 @@ def test_append_to_another_slots_page(ops, make, slots):
         assert ((got[b, : hi - lo] - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -9).all()
     ops.cache_append(cache, i32([64, 120]), 8, new, 1)   # slot 0 behind the shared page, slot 1 on the kept one
     assert ops.device_status(book.ws) == 0
+
+
+def test_handles_keep_their_tensors(ops):
+    """The C structs hold the tensors' addresses: another tensor in their place is refused, not forgotten."""
+    book = ops.PageTable.empty(2, 4, 8, 16)
+    cache = ops.PagedCache.e4m3(book, 8)
+    for handle, names in ((book, ("table", "refs", "page_size", "ws", "slots", "max_pages", "num_pages")),
+                          (cache, ("pages", "scales", "book", "block", "d"))):
+        for name in names:
+            held = getattr(handle, name)
+            with pytest.raises(AttributeError):
+                setattr(handle, name, held.clone() if isinstance(held, torch.Tensor) else held)
+            with pytest.raises(AttributeError):
+                delattr(handle, name)
+            assert getattr(handle, name) is held
+    book.table[0, 0] = 3                                 # their contents are the caller's
+    cache.scales.fill_(1.0)

@@ -8,7 +8,7 @@ import torch
 
 from oracle import csa_oracle as O
 from tests.parity import np64
-from tests.test_gpu_attn8 import BOUNDS, D, Plain, check_close, i32, make_cache, make_q, reference
+from tests.test_gpu_attn8 import D, Plain, check_close, i32, make_q, run_case
 
 pytestmark = pytest.mark.gpu
 
@@ -82,6 +82,126 @@ def test_infinite_sink_in_the_contiguous_form(ops, split):
     assert (outs[1][5] == 0).all()
     rest = [h for h in range(H) if h != 5]
     assert torch.equal(outs[0][rest], outs[1][rest])
+
+
+# ------------------------------------------------------------------------------------------------ hard rows
+
+
+@pytest.mark.parametrize("scale", [-0.5, 0.0, 1e-6, 3.0])
+def test_other_scales(ops, scale):
+    p = Split(ops, E=640)
+    want, tol, _ = p.want(scale=scale)
+    for form in FORMS:
+        for split in (True, False):
+            check_close(p.run(split, form, scale), want, tol, f"{form} split={split} scale={scale}")
+
+
+def test_lists_that_leave_little(ops):
+    """A list of 640 places, few of them taken: whole splits are left without a candidate."""
+    p = Split(ops, E=640)
+    p.idx.fill_(-1)
+    p.check(forms=("list",))                     # the window alone
+    p.idx[0, 0, 633] = 639
+    p.check(forms=("list",))
+    p.idx[0, 0, 3:9] = 42                        # the same entry six times counts six times
+    p.check(forms=("list",))
+    p.idx[0, 0, 200:] = -1                       # ends long before the list does
+    p.check(forms=("list",))
+    p.sink.fill_(-INF)
+    p.check(forms=("list",))
+
+
+@pytest.mark.parametrize("pages", [[0], [9], [2, 3, 4, 5], list(range(10))])
+def test_zero_scales_do_not_count(ops, pages):
+    """Some splits' rows, or every entry's, left out by a scale of zero."""
+    p = Split(ops, E=640)
+    t = p.cache.book.table[0].long()
+    for i in pages:
+        p.cache.scales[t[i]] = 0.0
+    p.check([e for e in range(640) if e // 64 not in pages])
+    p.sink.fill_(-INF)
+    p.check([e for e in range(640) if e // 64 not in pages])
+
+
+def test_extreme_magnitudes(ops):
+    """q and rows near the ends of their ranges; a page of tiny scales, a split of them, beside ordinary ones."""
+    p = Split(ops, E=640)
+    t = p.cache.book.table[0].long()
+    p.cache.scales[t[1]] = 2.0 ** -100
+    p.check()
+    for i in range(6):
+        p.cache.scales[t[i]] = 2.0 ** -100
+    p.check()
+    p.q[0, 0, 3] *= 2.0 ** -90
+    p.q[0, 0, 4] = 0
+    p.ring[0, 2] = 0
+    p.ring[0, 3] *= 2.0 ** -110
+    p.check()
+
+
+def test_what_is_not_a_number(ops):
+    """NaN and infinities reach the heads and queries that read them, and no others, in whichever split they lie."""
+    for page in (0, 4, 9):
+        p = Split(ops, E=640)
+        t = p.cache.book.table[0].long()
+        p.cache.pages.view(torch.uint8)[t[page], 5, 77] = 0x7F           # a NaN code
+        p.idx[p.idx // 64 == page] = -1
+        p.check([e for e in range(640) if e // 64 != page], forms=("list",))
+        p.idx[0, 0, 100] = 64 * page + 5
+        for split in (True, False):
+            for form in FORMS:
+                assert p.run(split, form)[:, 77].isnan().all()
+        p = Split(ops, E=640)
+        p.cache.scales[t[page], 1] = NAN
+        for split in (True, False):
+            for form in FORMS:
+                assert p.run(split, form).isnan().all()
+    p = Split(ops, E=640)
+    want, tol, _ = p.want()
+    p.q[0, 0, 9, 100], p.q[0, 0, 10, 100] = NAN, INF
+    rest = [h for h in range(128) if h not in (9, 10)]
+    for split in (True, False):
+        for form in FORMS:
+            out = p.run(split, form)
+            assert out[9].isnan().all() and out[10].isnan().all()
+            check_close(out[rest], want[rest], tol[rest], f"{form} split={split}")
+    p = Split(ops, E=640)
+    p.ring[0, 5, 5] = NAN
+    for split in (True, False):
+        for form in FORMS:
+            assert p.run(split, form).isnan().all()
+
+
+# ------------------------------------------------------------------------------------------------ every entry counts
+
+
+@pytest.mark.parametrize("B,S,H,W,page,block,pos,ratio", [
+    (1, 1, 128, 128, 64, 16, [5], 128),
+    (1, 1, 128, 128, 32, 1, [200002], 128),
+    (3, 1, 64, 128, 64, 32, [127, 128, 9000], 128),
+    (1, 1, 128, 16, 16, 2, [19999], 4),
+    (75, 1, 128, 128, 1024, 64, [5000 + i for i in range(75)], 4),
+    (1, 50, 32, 128, 64, 16, [350], 4),
+    (1, 39, 128, 100, 64, 16, [380], 4),
+])
+def test_range_in_32_bits(ops, B, S, H, W, page, block, pos, ratio):
+    """The range form's fp32 output, held to the mean square of independent roundings too."""
+    run_case(ops, B=B, S=S, H=H, W=W, page=page, block=block, pos=pos, ratio=ratio, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("E", [300, 640, 1000, 5000])
+def test_no_entry_is_missing(ops, E):
+    """The mean square tells a range that ends one entry early from the whole one."""
+    p = Split(ops, E=E)
+    want, tol, var = p.want(range(E))
+    limit = 2.0 ** -16 * var                     # independent roundings of the weights, each within 2^-8 of itself
+    short = p.want(range(E - 1))[0]
+    assert np.mean((short - want) ** 2) > 2 * limit
+    for form in FORMS if E <= 2048 else ("range",):
+        for split in (True, False):
+            out = p.run(split, form)
+            check_close(out, want, tol, f"{form} split={split}")
+            assert np.mean((np64(out) - want) ** 2) <= limit
 
 
 # ------------------------------------------------------------------------------------------------ long tails

@@ -49,6 +49,11 @@ def load_peaks():
     return dict(hbm_gbs=6650.0, bf16_tflops=1590.0, bf16_tflops_sustained=1400.0, source="fallback")
 
 
+# What the kernels of the decode step are compiled from (under csrc/): their .cu file and every header that it includes.
+KERNEL_SOURCES = {"indexer": ["indexer.cu", "compress_decode.cuh", "kernels.cuh", "ptx.cuh", "rope.cuh", "status.cuh"],
+                  "attention": ["attn.cu", "attn_util.cuh", "kernels.cuh", "ptx.cuh", "rope.cuh", "status.cuh"]}
+
+
 def kernel_hash(files):
     """Hash of the kernel's sources with comments and blank space removed: a recorded ncu capture
     stays valid across comment edits and is invalidated by any change to the code."""
@@ -740,8 +745,7 @@ def main(argv=None):
     dom = max(("indexer", "attention") if wl.has_indexer else ("attention",), key=lambda n: r["stage_ms"][n])
     bytes_launch = per_q[dom] * wl.B
     achieved = bytes_launch / (r["stage_ms"][dom] * 1e-3) / 1e9
-    files = {"indexer": ["indexer.cu", "compress_decode.cuh", "ptx.cuh", "kernels.cuh"],
-             "attention": ["attn.cu", "ptx.cuh", "kernels.cuh", "rope.cuh"]}[dom]
+    files = KERNEL_SOURCES[dom]
     total_bytes = sum(per_q.values()) * wl.B
     line = {
         "metric": METRIC,

@@ -118,8 +118,10 @@ __device__ __forceinline__ bool others_page(const AppendParams& P, int b, long l
 // A CTA takes one unit of max(block, 16) entries (a block's rows share its scale, and a unit lies inside
 // one page); a warp takes a row at a time, 16 dims a lane, and keeps it in registers between the block's maximum
 // and the rounding, so every row is read once. Bound by latency: the position, then rows and page, then the page's holders and the
-// block's scale, the codes. B200: one entry of 64 requests 2.5 us, 8192 entries (8.4 MB read, 4.2 written) 4.3 (with 16 warps a
-// CTA, whose registers leave two CTAs an SM, 2 us more).
+// block's scale, the codes. B200, blocks of 16: one entry of 64 requests 2.5 us, 8192 entries of four (8.4 MB read, 4.2 written) 4.3,
+// 32768 of one 11.7 (2.7, 4.6 and 10.3 without the look at the holders and with the scale read behind the rows; with 16 warps a CTA
+// 2 us more). Four CTAs an SM (64 registers; two for blocks of 64): for blocks of 16, five of 48 take 5.1 us at 8192 entries, for
+// blocks of 32 three of 80 take 4.7 instead of 4.4.
 //   scale of a block = the least power of two 2^k with max |x| <= 448 * 2^k over its rows, and never less
 //   than before: when new rows raise it, the earlier rows' codes are rounded again to the new step (by an exact
 //   power of two; only codes below e4m3's normal range lose bits).
@@ -127,7 +129,7 @@ __device__ __forceinline__ bool others_page(const AppendParams& P, int b, long l
 // exact in bf16. A row with a value that is not finite makes its block's scale NaN.
 // kMax: rows a warp takes, unit / 8.
 template <int kMax>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendParams P) {
+__global__ void __launch_bounds__(kAppendThreads, kMax == 8 ? 2 : 4) cache_append_kernel(AppendParams P) {
   __shared__ int row_k[kAppendMaxUnit];
   __shared__ float s_new[kAppendMaxUnit], s_old[kAppendMaxUnit];
   pdl_wait();
@@ -165,9 +167,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendPara
   const long long row0 = ((long long)page << P.page_shift) + (u0 & ((1 << P.page_shift) - 1));
   // The page's holders, and the scale so far of the block that the thread's row begins: on their way beside the rows.
   const int held = P.refs[page], r0 = threadIdx.x, block = 1 << P.block_shift;
-  float* sp = P.scales + ((row0 + r0) >> P.block_shift);
   const bool begins = r0 < P.unit && (r0 & (block - 1)) == 0;
-  const float old = begins && u0 + r0 < e0 ? *sp : 0.f;  // (a block without earlier rows has none)
+  const float old = begins && u0 + r0 < e0 ? P.scales[(row0 + r0) >> P.block_shift] : 0.f;  // (a block without earlier rows has none)
 #pragma unroll
   for (int i = 0; i < kMax; ++i) {
     const int r = warp + kWarps * i;
@@ -185,11 +186,6 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendPara
       if (lane == 0) row_k[r] = k;
     }
   }
-  // Rows are not written over another slot's.
-  if (held > 1 && __syncthreads_or(others_page(P, b, lp, page, threadIdx.x, kAppendThreads))) {
-    if (threadIdx.x == 0) record_status(P.status, CSA_DEV_BOUNDS);
-    return;
-  }
   __syncthreads();
   // A thread a row of the unit; the first of each block settles its scale.
   if (threadIdx.x < (unsigned)P.unit) {  // (16, 32 or 64 of them: whole half warps)
@@ -203,10 +199,15 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendPara
       if (old != old || old > s) s = old;
       s_old[r >> P.block_shift] = old;
       s_new[r >> P.block_shift] = k == -1000 ? 0.f : s;  // 0: nothing new in the block
-      if (k != -1000) *sp = s;
     }
   }
   __syncthreads();
+  // Nothing is written over another slot's rows. (Looked at here, behind both barriers, the holders have arrived.)
+  if (held > 1 && __syncthreads_or(others_page(P, b, lp, page, threadIdx.x, kAppendThreads))) {
+    if (threadIdx.x == 0) record_status(P.status, CSA_DEV_BOUNDS);
+    return;
+  }
+  if (begins && s_new[r0 >> P.block_shift] != 0.f) P.scales[(row0 + r0) >> P.block_shift] = s_new[r0 >> P.block_shift];
 #pragma unroll
   for (int i = 0; i < kMax; ++i) {
     const int r = warp + kWarps * i;
@@ -339,7 +340,9 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(ReadParams P) 
 // memory a reservation took 7.2 us instead of 3.7). Up to kPagesSmall places and pages one CTA is quicker, beyond a
 // cluster of 8; B200, back to back: 4 slots x 8 places, 64 pages: reserve 2.6 (cluster: 3.5), fork 5.0 (7.2), compact
 // 2.8 (4.5) us; 64 x 32, 2048 pages: 3.3 (3.7), 6.9 (8.5), 3.8 (4.9); 64 x 64, 4096 pages: 4.0 (3.7), 8.9 (9.0), 4.9 (5.1); one CTA
-// at 64 x 128, 8192 pages: 6.2, 17.7 and 11.0 against the cluster's 3.9, 9.4 and 5.3. What depends on a slot alone is
+// at 64 x 128, 8192 pages: 6.2, 17.7 and 11.0 against the cluster's 3.9, 9.4 and 5.3 (a fork takes 0.1 more since it looks for
+// places without a page). At a million tokens a slot: 8 x 4096 places, 16384 pages: 7.1, 17.2, 9.6; 64 x 4096, 131072 pages: 33.0,
+// 92.0, 58.3. What depends on a slot alone is
 // worked out first, by every CTA in its own shared memory (S), or for more than kPagesSmallSlots slots once, in the workspace.
 
 // f(i, g(i)) for i = first, first + step, ... below n, with four g under way.
@@ -627,8 +630,8 @@ CSA_PAGES_KERNELS(pages_compact)
 
 // The moves of a fork or a compaction, in every pool: work unit = (move, chunk of a pool's page), 16 bytes a thread
 // and load, four loads in flight. Sources and destinations of one call never overlap. Bound by DRAM: a page's bytes
-// are read and written once. B200: half of 16384 pages of 32 KB to the front in 41 us, 5.2 TB/s of traffic, 0.80 of the HBM
-// copy rate (chunks of 8 or 32 KB: 43).
+// are read and written once. B200: 4016 pages of 32 KB (half of 16384 live) to the front in 41.3 us, 263 MB read and written at
+// 6.4 TB/s, 0.97 of the HBM copy rate (chunks of 8 or 32 KB: 43).
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(CopyParams P) {
   pdl_wait();
   pdl_trigger();

@@ -429,7 +429,7 @@ typedef struct {
 
 /*
  * csa_cache_append -- the entries that a segment of S tokens completes, from `rows` (where csa_compress leaves them: entry g
- * of request b at rows + b*rows_bstride + g*d; one such buffer serves every layer in turn) into the pages. For
+ * of request b at rows + b*rows_bstride + g*d, so a buffer as long as the longest request; one serves every layer in turn) into the pages. For
  * request b these are entries start_pos[b]/ratio .. (start_pos[b]+S)/ratio - 1; a negative start_pos marks a
  * request to skip. 8-bit caches: a block's scale becomes the least power of two 2^k (k >= -100) with max |x| <= 448 * 2^k over its
  * rows, and never less than it was while the block has earlier rows (rows of entries below start_pos/ratio), whose codes are
@@ -445,7 +445,8 @@ CSA_API int csa_cache_append(const csa_page_table* pt, const csa_paged_cache* ca
                              void* ws, size_t ws_bytes, void* stream);
 
 /*
- * csa_cache_read -- entries idx[b, i] of each request as bf16: out[b, i, :] = code * scale (exact for power-of-two scales). An
+ * csa_cache_read -- entries idx[b, i] of each request as bf16: out[b, i, :] = code * scale (exact for power-of-two scales, but that
+ * rows appended with 2^128 - 2^123 or more read as infinity: their nearest code stands for 2^128). An
  * index of -1 leaves its row of `out` as it was; one whose page is not mapped does too, and records CSA_ERR_BOUNDS.
  *   idx dev int32 [B, n]; out dev bf16 [B, n, d], 16-byte aligned.
  */
@@ -517,10 +518,12 @@ typedef struct {
  *   segment's queries are all there if ring_cap >= window + S - 1 (the caller's choice, not checked).
  *   Pointers 16-byte aligned. ws: csa_workspace_size(CSA_WS_SPARSE_ATTN, ...) / CSA_WS_HCA_ATTN, or only its
  *   status word (slower for few queries).
- * Precision: the softmax weights of the numerator are held in two 8-bit pieces. A weight (times its block's scale) is off by at
- * most 2^-8 of itself down to 2^-9 of the row's largest, by more below: 2^-3 of itself at 2^-14. One below 2^-20 of the largest adds
- * nothing for up to 26 tiles of 64 candidates; for longer lists that limit falls with the number of tiles, to 2^-25 from 854 on, so that a
- * long tail is not lost. The denominator is the sum of the whole weights. q, window rows: see csrc/attn8.cu.
+ * Precision, also of an fp32 output: the softmax weights of the numerator are held in two 8-bit pieces (those of csa_sparse_attn in two
+ * bf16 ones, 2^-16). A weight (times its block's scale) is off by at most 2^-8 of itself down to 2^-9.75 of the row's largest, by more
+ * below: 2^-3 of itself from 2^-13.75 on. One below 2^-20.75 of the largest adds nothing for up to 26 tiles of 64 candidates; that limit
+ * falls with the number of tiles, to 2^-25.75 from 854 on, so that a long tail is not lost. So scales far apart cost the entries of
+ * small scale their bits. The denominator sums the whole weights, of entries whose scale is above 2^-100 of the largest. q is exact down
+ * to 2^-14 of a head's largest element and off by at most 2^-21 of it below, a window row to 2^-10 and 2^-17 of its largest.
  * A selected entry that is not visible at t, a visible one (range form) beyond the table, or an entry whose page is
  * not mapped is skipped and records CSA_ERR_BOUNDS.
  */

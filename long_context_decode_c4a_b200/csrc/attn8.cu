@@ -43,10 +43,10 @@
 //     PV(j - 1) (ack), raises it if its own scores ask for it, and hands it on before it forms P.
 // Split-candidate mode (few queries): as in attn.cu; attn_combine_kernel merges the partials.
 //
-// One B200, in a graph: 64 requests at 32K (1024 of 8192 entries and 128 window rows each) 42.2 us, 0.28 of the time that the
-// operations need at the dense bf16 rate and 0.21 of the HBM copy rate; a segment of 2000 queries 1092 us (0.33 of the
-// former); 24 requests of 1500 entries 36.4 us; one request of 39 entries 19.4 us. No unit is near its limit (tensor
-// pipe 23 %, issue slots 27 %): bound by the way of a tile through its stations, gather to PV, that six slots cover, and by
+// One B200, in a graph: 64 requests at 32K (1024 of 8192 entries and 128 window rows each) 42.8 us, 0.27 of the time that the
+// operations need at the dense bf16 rate and 0.21 of the HBM copy rate; a segment of 2000 queries 1105 us (0.33 of the
+// former); 24 requests of 1500 entries 36.8 us; one request of 39 entries 19.8 us. (Fewer heads than 128 are padded to 128: 16 heads
+// of the first case take 40.3 us.) No unit is near its limit (tensor pipe 23 %, issue slots 26 %): bound by the way of a tile through its stations, gather to PV, that six slots cover, and by
 // 5 us before the first scores (list, q and its split) and 3 after the last PV.
 
 #include <math_constants.h>
@@ -81,7 +81,7 @@ constexpr uint32_t kScoreCol = 128, kPCol = 192, kOCol = 256;
 // far below the largest: P below 2^-14 is off by up to 2^-22, its pieces' steps there, which J tiles can add up to
 // 64 J 2^(head - 22) of the largest weight. So head is what keeps that below 2^-7 (P's own precision is 2^-8): kHeadMost up to 26
 // tiles, then a binade less for each doubling, and none from 854 tiles on (54592 candidates a pair), beyond which the bound grows with
-// the number of tiles. Less for few tiles would cost: 64 queries of 20 tiles took 42.6 us at 4.25, 44.4 at 3.7, as one of a
+// the number of tiles. Less for few tiles would cost: 64 queries of 20 tiles took 42.8 us at 4.25, 44.4 at 3.7, as one of a
 // warp's 32 heads needs a rescale more often; on long lists new maxima are rare.
 constexpr float kHeadMost = 4.25f, kHeadLeast = -0.75f, kOver = 0.75f;
 static_assert(kAttn8Threads == 32 * (kSoftWarp + 8), "warp roles");

@@ -553,7 +553,9 @@ class PageTable(_Handle):
 
 class PagedCache(_Handle):
     """A cache behind a page table: pages [num_pages, page_size, 512] of e4m3 codes with scales [num_pages,
-    page_size // block] (fp32, one per block of rows), or pages [num_pages, page_size, d] of bf16 rows without scales."""
+    page_size // block] (fp32, one per block of rows), or pages [num_pages, page_size, d] of bf16 rows without scales.
+    A new 8-bit cache has scales of zero, and the attention leaves rows of scale zero out of the softmax: an entry that is
+    visible, mapped and was never appended does not count, and nothing reports it."""
 
     def __init__(self, book: PageTable, pages: torch.Tensor, scales: Optional[torch.Tensor] = None):
         if pages.dim() != 3 or pages.shape[0] != book.num_pages or pages.shape[1] != book.page_size:
